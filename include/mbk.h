@@ -282,6 +282,114 @@ void mbk_destroy(mbk_handle *h);
 int mbk_decode_step_static(const mbk_config *cfg, const mbk_weights *weights, void *kv_cache, int32_t token_id,
                            int32_t position, float *logits_out, void *stream);
 
+/* ---- a KV cache held in 4 bits ----
+ * (Not a counterpart of anything in the MegaBake pages: it exists for callers of this library.)
+ *
+ * Operators on a pool of pages whose rows hold every element in 4 bits: append, read, attention and
+ * eviction by accumulated attention weight.  They need no handle.  (A decoder whose prefill and batch
+ * steps run on such a pool: mbk_create_kv4.)
+ *
+ * Format.  A row (the K or the V of one token and KV head, head_dim elements) is cut into groups of
+ * 64 elements x:  lo = fp16(min x), scale = fp16((max x - min x) / 15), both rounded from fp32;
+ * code = (x - lo) / scale rounded to nearest even, clamped to 0 .. 15 (0 when scale is 0).  The row
+ * stands for lo + scale * code.  Elements beyond +-65504 are taken as +-65504; a NaN makes its whole
+ * group NaN.  A row costs 36 bytes for head_dim 64 and 72 for 128 (bf16: 128 and 256).
+ *
+ * Pool: [num_pages][n_layers][n_kv_heads][page_size / 32] blocks.  A block holds 32 rows of one KV
+ * head: K codes [32][head_dim / 2] (element 2 b in the low half of byte b), K pairs
+ * [32][head_dim / 64] of fp16 (scale, lo), then V codes and V pairs, and with track = 1 the rows'
+ * positions int32 [32] and accumulated attention weights fp32 [32].
+ *
+ * Ownership: the caller owns the pool, the batch's arrays, the workspace and every output.
+ * Threading / streams: a call only enqueues work on `stream` of cfg->device (the calling thread's current
+ * device is left as it was).  Calls are independent of one another: they may run at the same time on
+ * several streams when they have different workspaces and outputs and do not write the same pool rows.  No call
+ * allocates, copies from the host or synchronises, so every call can be captured into a graph; a graph
+ * reads rows, offsets, positions and tables again at every replay.
+ * Errors: host checks return MBK_ERR_INVALID_ARG and launch nothing.  What lies in device arrays
+ * cannot be checked on the host: a page number outside the pool and a batch entry outside its bounds
+ * are found by the kernels, which touch nothing there (rows of a bad page count as not visible and
+ * read as zero, a bad sequence has no tokens) and OR a bit into *status. */
+
+#define MBK_KV4_MAX_SEQS 1024 /* sequences of a call */
+#define MBK_KV4_MAX_EVICT_ROWS (1 << 20) /* rows of a sequence that is cut */
+#define MBK_KV4_BAD_PAGE 1    /* status bit: a page table entry outside [0, num_pages) */
+#define MBK_KV4_BAD_BATCH 2   /* status bit: rows, offsets or a token count outside their bounds */
+
+enum { MBK_KV4_FP32 = 0, MBK_KV4_BF16 = 1 }; /* type of k, v, q and out */
+
+typedef struct {
+  int32_t device;
+  int32_t n_layers, n_heads, n_kv_heads, head_dim; /* head_dim 64 or 128; at most 16 query heads per KV head */
+  int32_t num_pages;
+  int32_t page_size; /* rows of a page: a power of two, 32 at least */
+  int32_t max_pages; /* entries of a sequence's page table */
+  int32_t track;     /* 1: rows carry a position and an accumulated weight (for mbk_kv4_evict) */
+} mbk_kv4_config;
+
+/* The tokens of one call.  Sequence s has rows[s] cache rows, of which the last
+ * offsets[s + 1] - offsets[s] belong to its new tokens (append stores them, attention queries from
+ * them); its token arrays are rows offsets[s] .. of k, v, q and out.  A sequence may have no new token (an idle
+ * slot).  All pointers are DEVICE pointers; the four bounds are host values. */
+typedef struct {
+  int32_t n_seq;            /* 1 .. MBK_KV4_MAX_SEQS */
+  int32_t n_tokens;         /* rows of k, v, q and out (offsets[n_seq] at most this; rows behind it are not touched) */
+  int32_t max_count;        /* no sequence has more new tokens */
+  int32_t max_rows;         /* no sequence has more rows; at most max_pages * page_size */
+  const int32_t *offsets;   /* [n_seq + 1] */
+  const int32_t *rows;      /* [n_seq] */
+  const int32_t *positions; /* [n_seq] position of the first new token, or NULL: the index of its row */
+  const int32_t *tables;    /* [n_seq][max_pages] page of rows q * page_size .. */
+  int32_t *status;          /* one word, or NULL */
+} mbk_kv4_batch;
+
+/* Bytes of the pool of a configuration, or MBK_ERR_INVALID_ARG. */
+int64_t mbk_kv4_pool_bytes(const mbk_kv4_config *cfg);
+
+/* Stores the new tokens' rows of `layer`: k and v are [n_tokens][n_kv_heads][head_dim] in `dtype`, with
+ * `ld` elements between tokens (16-byte aligned, ld a multiple of 16 bytes; K already rotated).
+ * A tracked pool's rows get their token's position and a weight of zero.  No two
+ * sequences of a call may have the same page among those that it writes. */
+int mbk_kv4_append(const mbk_kv4_config *cfg, void *pool, int32_t layer, const mbk_kv4_batch *batch, const void *k,
+                   const void *v, int64_t ld, int32_t dtype, void *stream);
+
+/* The reverse: the values that the new tokens' rows stand for (a batch whose tokens are all its rows
+ * reads the whole cache).  k and v as in mbk_kv4_append, written. */
+int mbk_kv4_read(const mbk_kv4_config *cfg, const void *pool, int32_t layer, const mbk_kv4_batch *batch, void *k, void *v,
+                 int64_t ld, int32_t dtype, void *stream);
+
+/* Attention of the new tokens over their sequences' rows of `layer`: token i of a sequence with c new
+ * tokens and R rows sees rows r <= R - c + i, and of these with window > 0 only those whose position is
+ * less than `window` before its own.  Positions are the stored ones (track = 1) or the row's index.
+ *   s = scale * q . k_r;  cap > 0: s = cap * tanh(s / cap);  slopes: s += slopes[head] * (pos_r - pos_i)
+ *   out = sum_r softmax(s)_r v_r;  zero for a token that sees no row
+ * q and out: [n_tokens][n_heads][head_dim] in `dtype` with ldq, ldo elements between tokens (alignment as
+ * append's).  Query head h reads KV head h / (n_heads / n_kv_heads).  slopes: DEVICE fp32 [n_heads] or NULL.
+ * accumulate (track = 1 only): adds to each row's weight the sum of softmax(s)_r over the sequence's new tokens and
+ * the KV head's query heads.
+ * Numerics: fp32 throughout for fp32 (operands of the tensor cores as fp16 pairs of 22 bits); for bf16 the
+ * softmax weights are rounded to fp16.  Results do not depend on anything but the inputs and the GPU (no atomics).
+ * workspace: mbk_kv4_attention_workspace(cfg, batch) bytes, 16-byte aligned, contents arbitrary. */
+int64_t mbk_kv4_attention_workspace(const mbk_kv4_config *cfg, const mbk_kv4_batch *batch);
+int mbk_kv4_attention(const mbk_kv4_config *cfg, void *pool, int32_t layer, const mbk_kv4_batch *batch, const void *q,
+                      int64_t ldq, void *out, int64_t ldo, int32_t dtype, float scale, float cap, const float *slopes,
+                      int32_t window, int32_t accumulate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Eviction (track = 1): in each of layers [layer, layer + n_layers) and each KV head, of a sequence's
+ * rows[s] rows at most `keep` are kept: first those with a position >= next_pos[s] - recent, then those of the
+ * largest accumulated weight, the lower row first among equals (NaN counts as 0).  Kept rows below `keep`
+ * stay where they are and the j-th row that became free gets the j-th kept row from above, so the order of
+ * rows changes; their positions and weights go with them.  rows_out[s] = min(rows[s], keep) (it may be
+ * rows itself).  out_tables NULL: in place; pages behind the first ceil(keep / page_size) are then free.
+ * out_tables [n_seq][out_pages]: the kept rows are written to these pages of the pool instead and the old
+ * ones stay as they are (pages that several sequences share); no page may be in both tables.
+ * workspace: mbk_kv4_evict_workspace bytes, 16-byte aligned. */
+int64_t mbk_kv4_evict_workspace(const mbk_kv4_config *cfg, int32_t n_layers, int32_t n_seq, int32_t keep);
+int mbk_kv4_evict(const mbk_kv4_config *cfg, void *pool, int32_t layer, int32_t n_layers, int32_t n_seq, int32_t max_rows,
+                  const int32_t *rows, const int32_t *tables, const int32_t *next_pos, int32_t keep, int32_t recent,
+                  const int32_t *out_tables, int32_t out_pages, int32_t *rows_out, int32_t *status, void *workspace,
+                  int64_t workspace_bytes, void *stream);
+
 /* ---- diagnostics (for tests and profiling; not needed to decode) ---- */
 
 /* Residual stream of the most recently COMPLETED step (synchronise its stream first), copied to the

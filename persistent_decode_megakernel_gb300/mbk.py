@@ -29,7 +29,8 @@ EXPORTED = ("mbk_create", "mbk_decode_step", "mbk_decode_step_host", "mbk_kv_fil
             "mbk_error_string", "mbk_destroy", "mbk_plan_check", "mbk_debug_taps", "mbk_debug_plan",
             "mbk_trace_enable", "mbk_trace_read", "mbk_debug_inject", "mbk_decode_step_static", "mbk_decode_steps",
             "mbk_decode_greedy", "mbk_create_paged", "mbk_set_page_table", "mbk_quantize_fp8", "mbk_prefill",
-            "mbk_debug_prefill_inject", "mbk_plan_simulate", "mbk_batch_step")
+            "mbk_debug_prefill_inject", "mbk_plan_simulate", "mbk_batch_step", "mbk_kv4_pool_bytes", "mbk_kv4_append",
+            "mbk_kv4_read", "mbk_kv4_attention_workspace", "mbk_kv4_attention", "mbk_kv4_evict_workspace", "mbk_kv4_evict")
 TASK_TYPES = {1: "qkv", 2: "attn", 3: "oproj", 4: "gateup", 5: "down", 6: "lmhead"}
 TRACE_STAMPS = 8  # per task: begin, inputs ready, end, first weight stage, four phase marks
 
@@ -60,6 +61,21 @@ class MbkLayerWeights(ctypes.Structure):
 class MbkWeights(ctypes.Structure):
     _fields_ = [("embed", ctypes.c_void_p), ("final_norm", ctypes.c_void_p),
                 ("layers", ctypes.POINTER(MbkLayerWeights))]
+
+
+MBK_KV4_FP32, MBK_KV4_BF16 = 0, 1
+MBK_KV4_BAD_PAGE, MBK_KV4_BAD_BATCH = 1, 2
+MBK_KV4_MAX_SEQS, MBK_KV4_MAX_EVICT_ROWS = 1024, 1 << 20
+
+
+class MbkKv4Config(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("device", "n_layers", "n_heads", "n_kv_heads", "head_dim", "num_pages", "page_size",
+                                              "max_pages", "track")]
+
+
+class MbkKv4Batch(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("n_seq", "n_tokens", "max_count", "max_rows")] + \
+               [(k, ctypes.c_void_p) for k in ("offsets", "rows", "positions", "tables", "status")]
 
 
 class MbkPlanInfo(ctypes.Structure):
@@ -139,6 +155,21 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.mbk_debug_inject.restype = ctypes.c_int
         lib.mbk_decode_step_static.argtypes = [ctypes.POINTER(MbkConfig), ctypes.POINTER(MbkWeights), vp, i32, i32, vp, vp]
         lib.mbk_decode_step_static.restype = ctypes.c_int
+        i64, f32, kcfg, kbatch = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(MbkKv4Config), ctypes.POINTER(MbkKv4Batch)
+        lib.mbk_kv4_pool_bytes.argtypes = [kcfg]
+        lib.mbk_kv4_pool_bytes.restype = i64
+        lib.mbk_kv4_append.argtypes = [kcfg, vp, i32, kbatch, vp, vp, i64, i32, vp]
+        lib.mbk_kv4_append.restype = ctypes.c_int
+        lib.mbk_kv4_read.argtypes = [kcfg, vp, i32, kbatch, vp, vp, i64, i32, vp]
+        lib.mbk_kv4_read.restype = ctypes.c_int
+        lib.mbk_kv4_attention_workspace.argtypes = [kcfg, kbatch]
+        lib.mbk_kv4_attention_workspace.restype = i64
+        lib.mbk_kv4_attention.argtypes = [kcfg, vp, i32, kbatch, vp, i64, vp, i64, i32, f32, f32, vp, i32, i32, vp, i64, vp]
+        lib.mbk_kv4_attention.restype = ctypes.c_int
+        lib.mbk_kv4_evict_workspace.argtypes = [kcfg, i32, i32, i32]
+        lib.mbk_kv4_evict_workspace.restype = i64
+        lib.mbk_kv4_evict.argtypes = [kcfg, vp, i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, i64, vp]
+        lib.mbk_kv4_evict.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
