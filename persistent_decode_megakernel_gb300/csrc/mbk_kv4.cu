@@ -15,7 +15,7 @@
 // ANDs (V, whose pairs run along rows: two more byte permutes per two words).  The tensor cores align a
 // subnormal's products by its exponent field (2^-14), so a code in the low end gives up 6 bits or more of
 // the sum's 24 (measured: 5e-5 off where 1e-6 was due); bf16 results do not notice, and for fp32 all codes
-// are brought four bits higher, by two more shifts, which leaves 2 bits lost at most.
+// are brought to the top of the subnormals, by three more shifts.
 //   fp32 queries keep fp32 accuracy: q is scaled to the top of fp16's range and split into
 // hi + lo fp16 (22 bits), the softmax weights likewise, and as a tile has 16 rows of which a KV head's
 // group fills at most 8, rows 0 .. 7 carry hi and rows 8 .. 15 lo: one mma does both.  bf16 queries
@@ -366,15 +366,15 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // The codes of a word as four operand registers (codes i and i + 4 in register i), in units of
-// 2^-24 (registers 1 and 3, with PRECISE all of them: 2^-20).
+// 2^-24 (16 times that in registers 1 and 3), with PRECISE of 2^-18.
 template <bool PRECISE>
 __device__ __forceinline__ void codes(uint32_t x, uint32_t (&r)[4]) {
-  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kTop = 0x03c003c0u;
   if (PRECISE) {
-    r[0] = (x << 4) & kHigh;
-    r[1] = x & kHigh;
-    r[2] = (x >> 4) & kHigh;
-    r[3] = (x >> 8) & kHigh;
+    r[0] = (x << 6) & kTop;
+    r[1] = (x << 2) & kTop;
+    r[2] = (x >> 2) & kTop;
+    r[3] = (x >> 6) & kTop;
   } else {
     const uint32_t x8 = x >> 8;
     r[0] = x & kLow;
@@ -437,7 +437,8 @@ template <int D, int MODE>
 struct QTile {
   static constexpr int kGroups = D / 64, NR = MODE == 2 ? 2 : 1, TILE = 8 * NR;
   uint32_t f[kGroups][4][4];
-  float mul[NR], add[kGroups][NR];  // score = scale_r * acc * mul + lo_r * add, natural logarithm's units
+  float mul[NR], add[kGroups][NR];  // score = scale_r * acc * mul + z_r * add, natural logarithm's units
+  float mid[kGroups];               // MODE 0: -7.5 sum(q) in acc's units; codes then count from their middle
   int limit[NR], qpos[NR];          // last visible row (-1: none), position
   float slope[NR];
 };
@@ -476,6 +477,7 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       t.add[g][nr] = sum * a.a.scale;
+      if (MODE == 0) t.mid[g] = sum;
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -484,15 +486,18 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
     ex = ex == 255 ? 140 : max(ex, 20);
     const float up = pow2i(140 - ex);
     t.mul[nr] = pow2i(ex - 140) * 16777216.f * a.a.scale;  // 2^24: the codes' subnormal unit
+    if (MODE == 0)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) t.mid[g] *= -7.5f * up / 16777216.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         // k step ks = 2 w + y: word w's code pairs (2 y, 2 y + 4) and (2 y + 1, 2 y + 5)
         const int w = ks >> 1, y = ks & 1;
-        const float up0 = MODE == 0 ? up * 0.0625f : up;  // every code 16 times too large, or every second
+        const float up0 = MODE == 0 ? up / 64.f : up, up1 = MODE == 0 ? up0 : up / 16.f;  // the codes' units
         const float e0 = x[g][8 * w + 2 * y] * up0, e1 = x[g][8 * w + 2 * y + 4] * up0;
-        const float e2 = x[g][8 * w + 2 * y + 1] * (up * 0.0625f), e3 = x[g][8 * w + 2 * y + 5] * (up * 0.0625f);
+        const float e2 = x[g][8 * w + 2 * y + 1] * up1, e3 = x[g][8 * w + 2 * y + 5] * up1;
         const uint32_t h0 = pack_half(e0, e1), h1 = pack_half(e2, e3);
         if (MODE == 0) {
           const float2 u0 = unpack_half(h0), u1 = unpack_half(h1);
@@ -531,7 +536,7 @@ __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& 
 #pragma unroll
     for (int n = 0; n < 4; ++n) {  // cache rows 8 tig' + 2 n + {0, 1} in columns 2 tig' + {0, 1}
       const uint2 w = *reinterpret_cast<const uint2*>(st + g * 1024 + place(8 * (gid >> 1) + 2 * n + (gid & 1)) + 8 * tig);
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      float c[4] = {MODE == 0 ? t.mid[g] : 0.f, MODE == 0 ? t.mid[g] : 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t b[4];
@@ -543,7 +548,7 @@ __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& 
       for (int j = 0; j < 2; ++j) {
         const float2 p = unpack_half(pr[(2 * n + j) * kGroups + g]);
         if (MODE == 0) {
-          sc[0][2 * n + j] += fmaf(p.x, (c[j] + c[2 + j]) * t.mul[0], p.y * t.add[g][0]);
+          sc[0][2 * n + j] += fmaf(p.x, (c[j] + c[2 + j]) * t.mul[0], fmaf(7.5f, p.x, p.y) * t.add[g][0]);
         } else {
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) sc[nr][2 * n + j] += fmaf(p.x, c[2 * nr + j] * t.mul[nr], p.y * t.add[g][nr]);
@@ -577,7 +582,7 @@ __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& 
 template <int D, int MODE>
 struct Acc {
   static constexpr int kGroups = D / 64, NR = MODE == 2 ? 2 : 1;
-  float o[kGroups][8][4];       // unit: 2^-24 2^(13 - e), 16 times that in the columns of 16-fold codes
+  float o[kGroups][8][4];       // units: the weights' 2^(13 - e) times those of codes()
   float m[NR], l[NR], z[kGroups][NR];
   int e;                        // exponent of the largest scale of V seen so far
   __device__ void clear() {
@@ -651,57 +656,67 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
     A.l[nr] = fmaf(A.l[nr], al[nr], ps);
   }
   const float f = pow2i(13 - A.e);
+  const float a0 = al[0] * unit, a1 = MODE == 2 ? al[NR - 1] * unit : a0;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
+    uint32_t af[2][4];
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) A.z[g][nr] *= al[nr];
-    // rescale only where some row's maximum or the unit moved (the common case is that none did)
-    const float a0 = al[0] * unit, a1 = MODE == 2 ? al[NR - 1] * unit : a0;
-    if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        A.o[g][j][0] *= a0;
-        A.o[g][j][1] *= a0;
-        A.o[g][j][2] *= a1;
-        A.o[g][j][3] *= a1;
-      }
-    }
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {  // cache rows 8 tig + 4 kk .. + 3
-      uint32_t af[4] = {0u, 0u, 0u, 0u};
+      if (MODE == 1) af[kk][1] = af[kk][3] = 0u;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int i = 4 * kk + 2 * y;
         const float2 p0 = unpack_half(pr[i * kGroups + g]), p1 = unpack_half(pr[(i + 1) * kGroups + g]);
+        const float z0 = MODE == 0 ? fmaf(p0.x, 7.5f, p0.y) : p0.y, z1 = MODE == 0 ? fmaf(p1.x, 7.5f, p1.y) : p1.y;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           // a weight of zero (a masked row) takes nothing of its row, NaN included
           const float w0 = sc[nr][i], w1 = sc[nr][i + 1];
           const float x0 = w0 > 0.f ? w0 * (p0.x * f) : w0, x1 = w1 > 0.f ? w1 * (p1.x * f) : w1;
-          A.z[g][nr] += w0 > 0.f ? w0 * p0.y : w0;
-          A.z[g][nr] += w1 > 0.f ? w1 * p1.y : w1;
+          A.z[g][nr] += w0 > 0.f ? w0 * z0 : w0;
+          A.z[g][nr] += w1 > 0.f ? w1 * z1 : w1;
           const uint32_t hi = pack_half(x0, x1);
           if (MODE == 0) {
             const float2 u = unpack_half(hi);
-            af[2 * y] = hi;
-            af[2 * y + 1] = pack_half(x0 - u.x, x1 - u.y);
+            af[kk][2 * y] = hi;
+            af[kk][2 * y + 1] = pack_half(x0 - u.x, x1 - u.y);
           } else {
-            af[2 * y + nr] = hi;
+            af[kk][2 * y + nr] = hi;
           }
         }
       }
-      const unsigned char* vb = st + S::kV + g * 1024 + 4 * gid;
-      uint32_t w[4];
+    }
+    // The block's share is summed from zero and added in fp32: the tensor cores' own sums are truncated, and
+    // over thousands of rows that bias showed (3e-4).  For fp32 they also start at -7.5 sum(p), so that
+    // codes count from their middle: sum p (code - 7.5) is of the output's size, sum p code many times that.
+    float mid[4] = {0.f, 0.f, 0.f, 0.f};
+    if (MODE == 0) {
+      constexpr uint32_t kMinus = 0x81e081e0u;  // -480 * 2^-24: -7.5 in units of 2^-18
+      mma_16816(mid, af[0], kMinus, kMinus);
+      mma_16816(mid, af[1], kMinus, kMinus);
+    }
+    const unsigned char* vb = st + S::kV + g * 1024 + 4 * gid;
+    uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(vb + place(8 * tig + 4 * kk + i));
+    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(vb + place(8 * tig + i));
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // codes 4 half .. + 3 of the word: dims 8 gid + 4 half ..
-        const uint32_t sel = half ? 0x7632u : 0x5410u;
-        uint32_t x[4], y[4];
-        codes<MODE == 0>(__byte_perm(w[0], w[1], sel), x);
-        codes<MODE == 0>(__byte_perm(w[2], w[3], sel), y);
+    for (int half = 0; half < 2; ++half) {  // codes 4 half .. + 3 of the word: dims 8 gid + 4 half ..
+      const uint32_t sel = half ? 0x7632u : 0x5410u;
+      uint32_t x[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_16816(A.o[g][4 * half + i], af, x[i], y[i]);
+      for (int i = 0; i < 4; ++i) codes<MODE == 0>(__byte_perm(w[2 * i], w[2 * i + 1], sel), x[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float c[4] = {mid[0], mid[1], mid[2], mid[3]};
+        mma_16816(c, af[0], x[0][i], x[1][i]);
+        mma_16816(c, af[1], x[2][i], x[3][i]);
+        float(&o)[4] = A.o[g][4 * half + i];
+        o[0] = fmaf(o[0], a0, c[0]);
+        o[1] = fmaf(o[1], a0, c[1]);
+        o[2] = fmaf(o[2], a1, c[2]);
+        o[3] = fmaf(o[3], a1, c[3]);
       }
     }
   }
@@ -738,7 +753,7 @@ __device__ __forceinline__ void finish(Acc<D, MODE>& A, const AttnArgs& a, const
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float o = MODE == 0 ? A.o[g][j][c] + A.o[g][j][2 + c] : A.o[g][j][2 * nr + c];
-          x[j] = fmaf(o, MODE == 0 || (j & 1) ? unit * 0.0625f : unit, z) * inv;
+          x[j] = fmaf(o, MODE == 0 ? unit / 64.f : (j & 1) ? unit / 16.f : unit, z) * inv;
         }
         if (!on) continue;
         if (dep != nullptr) {

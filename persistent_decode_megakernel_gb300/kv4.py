@@ -21,6 +21,13 @@ import torch
 
 from . import mbk
 
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of torch's current stream of a device."""
+    return torch._C._cuda_getCurrentRawStream(index)  # torch.cuda.current_stream makes an object first: 2 us more
+
+
 _DTYPES = {torch.float32: mbk.MBK_KV4_FP32, torch.bfloat16: mbk.MBK_KV4_BF16}
 
 
@@ -52,6 +59,7 @@ class Kv4Cache:
         self._cfg = ctypes.byref(self.cfg)
         self.lib = mbk.load_library()
         self.bytes = self._size(self.lib.mbk_kv4_pool_bytes(self._cfg), "mbk_kv4_pool_bytes")
+        self.index = device
         self.device = torch.device("cuda", device)
         if pool is None:
             pool = torch.zeros(self.bytes, dtype=torch.uint8, device=self.device)
@@ -78,13 +86,18 @@ class Kv4Cache:
         d = self.cfg.head_dim
         if not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype not in _DTYPES or t.shape != (n, heads, d):
             raise ValueError(f"{name}: an fp32 or bf16 tensor {(n, heads, d)} on {self.device}")
-        st, unit = t.stride(), 16 // t.element_size()
-        if st[2] != 1 or (heads > 1 and st[1] != d) or (n > 1 and (st[0] < heads * d or st[0] % unit != 0)) or t.data_ptr() % 16 != 0:
-            raise ValueError(f"{name}: heads and elements contiguous, tokens apart by a multiple of 16 bytes, 16-byte aligned")
-        return t.data_ptr(), st[0] if n > 1 else heads * d
+        p, ld = t.data_ptr(), heads * d
+        if not t.is_contiguous():
+            st, unit = t.stride(), 16 // t.element_size()
+            if st[2] != 1 or (heads > 1 and st[1] != d) or (n > 1 and (st[0] < ld or st[0] % unit != 0)):
+                raise ValueError(f"{name}: heads and elements contiguous, tokens apart by a multiple of 16 bytes")
+            ld = st[0] if n > 1 else ld
+        if p % 16 != 0:
+            raise ValueError(f"{name}: 16-byte aligned")
+        return p, ld
 
     def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _raw_stream(self.index)
 
     def batch(self, offsets, rows, tables, positions=None, n_tokens: Optional[int] = None, max_count: Optional[int] = None,
               max_rows: Optional[int] = None, status: Optional[torch.Tensor] = None) -> Kv4Batch:
