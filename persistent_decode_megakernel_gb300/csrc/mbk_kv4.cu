@@ -16,12 +16,13 @@
 // subnormal's products by its exponent field (2^-14), so a code in the low end gives up 6 bits or more of
 // the sum's 24 (measured: 5e-5 off where 1e-6 was due); bf16 results do not notice, and for fp32 all codes
 // are brought to the top of the subnormals, by three more shifts.
+//   The operands stand as S^T = K Q^T and O^T = V^T P^T: 16 cache rows (16 dims) are the rows of the tile
+// and the queries its 8 columns, so a KV head's few queries waste little.  The columns of S^T are
+// those of O^T, so running maxima, sums and rescaling stay in a lane's own columns; between the two
+// products P goes through one 8 x 8 transposition (movmatrix) per 8 rows.
 //   fp32 queries keep fp32 accuracy: q is scaled to the top of fp16's range and split into
-// hi + lo fp16 (22 bits), the softmax weights likewise, and as a tile has 16 rows of which a KV head's
-// group fills at most 8, rows 0 .. 7 carry hi and rows 8 .. 15 lo: one mma does both.  bf16 queries
-// need one fp16 each.
-//   The score tile of one mma is, register for register, the A operand of the next (the columns of S
-// are the k index of P V), so nothing is exchanged between lanes except the row maxima.
+// hi + lo fp16 (22 bits), the softmax weights likewise; up to 4 queries hold hi in columns 0 .. 3 and lo
+// in 4 .. 7, so that one mma does both, more take a second tile.  bf16 queries need one fp16 each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,13 +39,28 @@ namespace {
 constexpr int kRows = kKv4Rows;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Warps of an attention CTA and blocks in flight per warp (at least 2).  One CTA per SM: with head dim
-// 64 a warp fits 128 registers, so 16 of them; with 128 the output alone takes 64, so 8.
+// MODE: what a tile's columns hold.
+enum Mode {
+  BF16_8 = 0,   // 8 bf16 queries
+  BF16_16 = 1,  // 16 bf16 queries, two tiles
+  FP32_4 = 2,   // 4 fp32 queries: hi | lo
+  FP32_8 = 3,   // 8 fp32 queries, a tile of hi and one of lo
+};
+// FEAT: 0: one token per sequence, nothing but the scale; 1: with cap or bias; 2: anything.  Only the last
+// has rows that some columns of a tile see and others do not, whose NaNs must be kept from the others.
+
+// Warps of an attention CTA (one CTA per SM) and blocks in flight per warp, within 227 KB of shared
+// memory and 65,536 registers.
 constexpr int kMaxWarps = 16;
 template <int D, int MODE>
 struct Shape {
-  static constexpr int kWarps = D == 64 ? 16 : 8;
-  static constexpr int kStages = MODE == 2 ? 3 : 4;
+  static constexpr int kGroups = D / 64;
+  static constexpr int NT = MODE == BF16_16 || MODE == FP32_8 ? 2 : 1;  // tiles of 8 columns
+  static constexpr int NS = MODE == BF16_16 ? 2 : 1;                    // column sets with a softmax of their own
+  static constexpr int TILE = MODE == BF16_16 ? 16 : MODE == FP32_4 ? 4 : 8;
+  static constexpr bool kPrecise = MODE >= FP32_4;
+  static constexpr int kWarps = D == 64 ? 16 : NT == 2 ? 8 : 12;
+  static constexpr int kStages = D == 64 && MODE != BF16_16 ? 4 : 3;
 };
 
 __device__ __forceinline__ void flag(int32_t* status, int bit) {
@@ -256,6 +272,7 @@ struct AttnArgs {
   Kv4Batch b;
   Kv4Attn a;
   int layer, grp, grid_max, warps;
+  float cap2;    // 2 log2(e) / cap
   float* part;   // [grid][2][tile rows][d + 2] partial (o, m, l) of segments that several CTAs share
   float* lse;    // [n_tokens][nq] log2 of the softmax denominators (accumulate), or null
 };
@@ -360,10 +377,22 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = a b + c on a 16 x 8 x 16 tile of fp16 with fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// The transpose of the 8 x 8 matrix of 16-bit values of which this lane holds row gid, columns 2 tig, 2 tig + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// (a, b) += (c, d) in one instruction.
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b) : "f"(c), "f"(d));
 }
 // The codes of a word as four operand registers (codes i and i + 4 in register i), in units of
 // 2^-24 (16 times that in registers 1 and 3), with PRECISE of 2^-18.
@@ -396,10 +425,10 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // A stage of the ring in shared memory: per group of 64 dims, 32 rows of 32 bytes.  Lane (gid, tig) of
-// the mma fragments reads rows 8 tig .. 8 tig + 7 (so their pairs are 32 contiguous bytes); row r goes
-// to byte (r % 8) * 128 + ((r / 8) ^ 2 (r & 1)) * 32, which makes both the 8-byte reads of K (rows
-// 2 t + 8 i + {0, 1}) and the 4-byte reads of V (rows i + 8 tig) free of bank conflicts.
-__device__ __forceinline__ int place(int r) { return (r & 7) * 128 + (((r >> 3) ^ ((r & 1) << 1)) << 5); }
+// the mma fragments reads 8 bytes of K rows 4 gid + i (so its rows' pairs are contiguous) and 4 bytes of
+// V rows 8 tig + i; row r goes to byte (r % 8) * 128 + ((r / 8) ^ 2 (r / 4 % 2)) * 32, which makes both
+// free of bank conflicts.
+__device__ __forceinline__ int place(int r) { return (r & 7) * 128 + (((r >> 3) ^ ((r & 4) >> 1)) << 5); }
 
 template <int D>
 struct Stage {
@@ -431,53 +460,56 @@ __device__ __forceinline__ void fetch(uint32_t st, const uint8_t* blk, bool pos,
   if (pos && lane < 8) cp16(st + S::kPos + lane * 16, blk + pos_at(D) + lane * 16);
 }
 
-// Query rows of a tile as A fragments.  MODE 0: fp32 queries, 8 rows, hi in fragment rows 0 .. 7 and lo
-// in 8 .. 15; MODE 1: bf16 queries, 8 rows; MODE 2: bf16 queries, 16 rows.
+// The queries of a tile as B fragments, and per lane what belongs to its columns 2 tig and 2 tig + 1.
 template <int D, int MODE>
 struct QTile {
-  static constexpr int kGroups = D / 64, NR = MODE == 2 ? 2 : 1, TILE = 8 * NR;
-  uint32_t f[kGroups][4][4];
-  float mul[NR], add[kGroups][NR];  // score = scale_r * acc * mul + z_r * add, natural logarithm's units
-  float mid[kGroups];               // MODE 0: -7.5 sum(q) in acc's units; codes then count from their middle
-  int limit[NR], qpos[NR];          // last visible row (-1: none), position
-  float slope[NR];
+  using P = Shape<D, MODE>;
+  uint32_t f[P::kGroups][4][P::NT][2];
+  float mul[P::NS][2], add[P::kGroups][P::NS][2];  // score = scale_r * acc * mul + z_r * add, natural logarithm's units
+  float mid[P::kGroups][2];                        // fp32: -7.5 sum(q) in acc's units; codes count from their middle
+  int limit[P::NS][2], qpos[P::NS][2];             // last visible row (-1: none), position
+  float slope[P::NS][2];
 };
 
-template <int D, int MODE>
+// Query column of a lane's C column j of softmax set ns.
+template <int MODE>
+__device__ __forceinline__ int column(int tig, int ns, int j) {
+  return MODE == FP32_4 ? (2 * tig + j) & 3 : 8 * ns + 2 * tig + j;
+}
+
+template <int D, int MODE, int FEAT>
 __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, const SeqInfo& sq, int s, int h, int tile, int lane) {
-  constexpr int kGroups = D / 64, NR = QTile<D, MODE>::NR, TILE = 8 * NR;
+  using P = Shape<D, MODE>;
+  constexpr int kGroups = P::kGroups, NS = P::NS;
   const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    const int row = tile * TILE + gid + 8 * nr, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
+  for (int ns = 0; ns < NS; ++ns) {
+    // this lane: column gid, dims 16 tig .. + 15 of each group
+    const int col = MODE == FP32_4 ? gid & 3 : 8 * ns + gid;
+    const int row = tile * P::TILE + col, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
     const bool on = tok < sq.c;
-    t.limit[nr] = on ? sq.r - sq.c + tok : -1;
-    t.qpos[nr] = on ? (a.b.positions != nullptr ? a.b.positions[s] : sq.r - sq.c) + tok : 0;
-    t.slope[nr] = on && a.a.slopes != nullptr ? a.a.slopes[head] : 0.f;
-    float x[kGroups][16];
+    float x[kGroups][16], sum[kGroups];
     float mx = 0.f;
     const size_t at = (size_t)(sq.tok0 + tok) * a.a.ldq + (size_t)head * D + 16 * tig;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      float sum = 0.f;
+      sum[g] = 0.f;
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (on) {
-          if (MODE == 0) load8<float>(reinterpret_cast<const float*>(a.a.q) + at + 64 * g + 8 * v, y);
+          if (P::kPrecise) load8<float>(reinterpret_cast<const float*>(a.a.q) + at + 64 * g + 8 * v, y);
           else load8<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.a.q) + at + 64 * g + 8 * v, y);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[g][8 * v + i] = y[i];
           mx = fmaxf(mx, fabsf(y[i]));
-          sum += y[i];
+          sum[g] += y[i];
         }
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      t.add[g][nr] = sum * a.a.scale;
-      if (MODE == 0) t.mid[g] = sum;
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -485,217 +517,291 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
     int ex = (__float_as_int(mx) >> 23) & 255;
     ex = ex == 255 ? 140 : max(ex, 20);
     const float up = pow2i(140 - ex);
-    t.mul[nr] = pow2i(ex - 140) * 16777216.f * a.a.scale;  // 2^24: the codes' subnormal unit
-    if (MODE == 0)
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) t.mid[g] *= -7.5f * up / 16777216.f;
+    const float up0 = P::kPrecise ? up / 64.f : up, up1 = P::kPrecise ? up0 : up / 16.f;  // the codes' units
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         // k step ks = 2 w + y: word w's code pairs (2 y, 2 y + 4) and (2 y + 1, 2 y + 5)
         const int w = ks >> 1, y = ks & 1;
-        const float up0 = MODE == 0 ? up / 64.f : up, up1 = MODE == 0 ? up0 : up / 16.f;  // the codes' units
         const float e0 = x[g][8 * w + 2 * y] * up0, e1 = x[g][8 * w + 2 * y + 4] * up0;
         const float e2 = x[g][8 * w + 2 * y + 1] * up1, e3 = x[g][8 * w + 2 * y + 5] * up1;
         const uint32_t h0 = pack_half(e0, e1), h1 = pack_half(e2, e3);
-        if (MODE == 0) {
+        if (P::kPrecise) {
           const float2 u0 = unpack_half(h0), u1 = unpack_half(h1);
-          t.f[g][ks][0] = h0;
-          t.f[g][ks][1] = pack_half(e0 - u0.x, e1 - u0.y);
-          t.f[g][ks][2] = h1;
-          t.f[g][ks][3] = pack_half(e2 - u1.x, e3 - u1.y);
+          const uint32_t l0 = pack_half(e0 - u0.x, e1 - u0.y), l1 = pack_half(e2 - u1.x, e3 - u1.y);
+          if (MODE == FP32_4) {
+            t.f[g][ks][0][0] = gid < 4 ? h0 : l0;
+            t.f[g][ks][0][1] = gid < 4 ? h1 : l1;
+          } else {
+            t.f[g][ks][0][0] = h0;
+            t.f[g][ks][0][1] = h1;
+            t.f[g][ks][P::NT - 1][0] = l0;
+            t.f[g][ks][P::NT - 1][1] = l1;
+          }
         } else {
-          t.f[g][ks][nr] = h0;
-          t.f[g][ks][2 + nr] = h1;
-          if (NR == 1) t.f[g][ks][1] = t.f[g][ks][3] = 0u;
+          t.f[g][ks][ns][0] = h0;
+          t.f[g][ks][ns][1] = h1;
         }
       }
+    const float down = pow2i(ex - 140) * 16777216.f;  // 2^24: the codes' subnormal unit
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int from = 4 * (2 * tig + j);  // a lane of that column
+      t.mul[ns][j] = __shfl_sync(0xffffffffu, down, from) * a.a.scale;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float sg = __shfl_sync(0xffffffffu, sum[g], from);
+        t.add[g][ns][j] = sg * a.a.scale;
+        if (P::kPrecise) {
+          const float m = sg * (-7.5f / 16777216.f) * __shfl_sync(0xffffffffu, up, from);
+          t.mid[g][j] = MODE == FP32_4 && tig >= 2 ? 0.f : m;  // the lo columns start at zero
+        }
+      }
+      const int crow = tile * P::TILE + column<MODE>(tig, ns, j), ctok = crow / a.grp;
+      const bool con = ctok < sq.c;
+      t.limit[ns][j] = con ? sq.r - sq.c + ctok : -1;
+      if (FEAT > 0) {
+        t.qpos[ns][j] = con ? (a.b.positions != nullptr ? a.b.positions[s] : sq.r - sq.c) + ctok : 0;
+        t.slope[ns][j] = con && a.a.slopes != nullptr ? a.a.slopes[h * a.grp + crow - ctok * a.grp] : 0.f;
+      }
+    }
   }
 }
 
-// Scores of the tile against a staged block, in units of the base-2 logarithm; sc[nr][i] belongs to
-// fragment row gid + 8 nr and cache row 32 blk + 8 tig + i; -inf where the row is not visible.
-// FULL: every row of the block is visible to every query of the tile.
-template <int D, int MODE, bool EXTRA>
+// Scores of the tile against a staged block, in units of the base-2 logarithm: sc[ns][i][j] is cache row
+// 32 blk + 4 gid + i against the lane's column j of set ns; -inf where the row is not visible.
+// full: every row of the block is visible to every query of the tile (a window aside).
+template <int D, int MODE, int FEAT>
 __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& a, const unsigned char* st, int blk, bool full, int lane,
-                                       float (&sc)[QTile<D, MODE>::NR][8]) {
+                                       float (&sc)[Shape<D, MODE>::NS][4][2]) {
   using S = Stage<D>;
-  constexpr int kGroups = D / 64, NR = QTile<D, MODE>::NR;
+  using P = Shape<D, MODE>;
+  constexpr int kGroups = P::kGroups, NS = P::NS, NT = P::NT;
   const int gid = lane >> 2, tig = lane & 3;
+  uint32_t pr[kGroups * 4];
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sc[nr][i] = 0.f;
-  uint32_t pr[kGroups * 8];
-#pragma unroll
-  for (int i = 0; i < 2 * kGroups; ++i)
-    *reinterpret_cast<uint4*>(pr + 4 * i) = *reinterpret_cast<const uint4*>(st + S::kCodes + tig * (32 * kGroups) + 16 * i);
+  for (int i = 0; i < kGroups; ++i)
+    *reinterpret_cast<uint4*>(pr + 4 * i) = *reinterpret_cast<const uint4*>(st + S::kCodes + gid * (16 * kGroups) + 16 * i);
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {  // cache rows 8 tig' + 2 n + {0, 1} in columns 2 tig' + {0, 1}
-      const uint2 w = *reinterpret_cast<const uint2*>(st + g * 1024 + place(8 * (gid >> 1) + 2 * n + (gid & 1)) + 8 * tig);
-      float c[4] = {MODE == 0 ? t.mid[g] : 0.f, MODE == 0 ? t.mid[g] : 0.f, 0.f, 0.f};
+    for (int mt = 0; mt < 2; ++mt) {  // tile rows gid: cache row 4 gid + 2 mt; gid + 8: the next one
+      const uint2 w0 = *reinterpret_cast<const uint2*>(st + g * 1024 + place(4 * gid + 2 * mt) + 8 * tig);
+      const uint2 w1 = *reinterpret_cast<const uint2*>(st + g * 1024 + place(4 * gid + 2 * mt + 1) + 8 * tig);
+      float c[NT][4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        uint32_t b[4];
-        codes<MODE == 0>(k ? w.y : w.x, b);
-        mma_16816(c, t.f[g][2 * k], b[0], b[1]);
-        mma_16816(c, t.f[g][2 * k + 1], b[2], b[3]);
+        uint32_t x[4], y[4];
+        codes<P::kPrecise>(k ? w0.y : w0.x, x);
+        codes<P::kPrecise>(k ? w1.y : w1.x, y);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const uint32_t af[4] = {x[2 * z], y[2 * z], x[2 * z + 1], y[2 * z + 1]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t(&b)[2] = t.f[g][2 * k + z][nt];
+            if (k + z > 0) mma(c[nt], af, b[0], b[1], c[nt][0], c[nt][1], c[nt][2], c[nt][3]);
+            else if (P::kPrecise && nt == 0) mma(c[nt], af, b[0], b[1], t.mid[g][0], t.mid[g][1], t.mid[g][0], t.mid[g][1]);
+            else mma(c[nt], af, b[0], b[1], 0.f, 0.f, 0.f, 0.f);
+          }
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 p = unpack_half(pr[(2 * n + j) * kGroups + g]);
-        if (MODE == 0) {
-          sc[0][2 * n + j] += fmaf(p.x, (c[j] + c[2 + j]) * t.mul[0], fmaf(7.5f, p.x, p.y) * t.add[g][0]);
-        } else {
+      for (int i = 0; i < 2; ++i) {
+        const float2 p = unpack_half(pr[(2 * mt + i) * kGroups + g]);
+        const float z = P::kPrecise ? fmaf(7.5f, p.x, p.y) : p.y;
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) sc[nr][2 * n + j] += fmaf(p.x, c[2 * nr + j] * t.mul[nr], p.y * t.add[g][nr]);
-        }
+        for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float acc = c[ns][2 * i + j];
+            if (MODE == FP32_8) acc += c[NT - 1][2 * i + j];
+            if (MODE == FP32_4) acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+            const float x = fmaf(p.x, acc * t.mul[ns][j], z * t.add[g][ns][j]);
+            if (g == 0) sc[ns][2 * mt + i][j] = x;
+            else sc[ns][2 * mt + i][j] += x;
+          }
       }
     }
   }
-  const int r0 = blk * kRows + 8 * tig;
+  const int r0 = blk * kRows + 4 * gid;
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr)
+  for (int i = 0; i < 4; ++i) {
+    const int kpos = FEAT > 0 && a.g.track ? *reinterpret_cast<const int*>(st + S::kPos + 4 * (4 * gid + i)) : r0 + i;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float x = sc[nr][i];
-      bool see = full || r0 + i <= t.limit[nr];
-      if (EXTRA) {
-        if (a.a.cap > 0.f) {
-          // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap))): off by a few 2^-24 of cap
-          const float e = ex2(fminf(x * (2.f * kLog2e / a.a.cap), 126.f));
-          x = a.a.cap * (1.f - __fdividef(2.f, 1.f + e));
+    for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = sc[ns][i][j];
+        bool see = full || r0 + i <= t.limit[ns][j];
+        if (FEAT > 0) {
+          if (a.a.cap > 0.f) {
+            // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap))): off by a few 2^-24 of cap
+            const float e = ex2(fminf(x * a.cap2, 126.f));
+            x = a.a.cap * (1.f - __fdividef(2.f, 1.f + e));
+          }
+          const int gap = kpos - t.qpos[ns][j];
+          if (a.a.slopes != nullptr) x = fmaf(t.slope[ns][j], (float)gap, x);
+          if (FEAT == 2 && a.a.window > 0) see = see && gap > -a.a.window;
         }
-        const int kpos = a.g.track ? *reinterpret_cast<const int*>(st + S::kPos + 4 * (8 * tig + i)) : r0 + i;
-        const int gap = kpos - t.qpos[nr];
-        if (a.a.slopes != nullptr) x = fmaf(t.slope[nr], (float)gap, x);
-        if (a.a.window > 0) see = see && gap > -a.a.window;
+        sc[ns][i][j] = see ? x * kLog2e : -INFINITY;
       }
-      sc[nr][i] = see ? x * kLog2e : -INFINITY;
-    }
+  }
 }
 
-// Running softmax and output of a tile.
+// Running softmax and output of a tile.  The reference value m of a column is a maximum of its scores that
+// is only renewed when a score exceeds it by kSlack (a factor of 256 in the weight): until then no lane needs
+// to know another's maximum, and nothing is rescaled.
+constexpr float kSlack = 8.f;
+constexpr int kUnit = 6;  // weights are held as p * scale_r * 2^(kUnit - e): below 2^15
 template <int D, int MODE>
 struct Acc {
-  static constexpr int kGroups = D / 64, NR = MODE == 2 ? 2 : 1;
-  float o[kGroups][8][4];       // units: the weights' 2^(13 - e) times those of codes()
-  float m[NR], l[NR], z[kGroups][NR];
-  int e;                        // exponent of the largest scale of V seen so far
+  using P = Shape<D, MODE>;
+  float o[P::kGroups][4][P::NT][4];  // dims 8 gid + 2 mt + {0, 1}, columns 2 tig + {0, 1}; units: 2^(kUnit - e) times those of codes()
+  float m[P::NS][2], l[P::NS][2], z[P::kGroups][P::NS][2];  // l and z: this lane's rows only
+  int e;                             // exponent of the largest scale of V seen so far
   __device__ void clear() {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < P::kGroups; ++g)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[g][j][k] = 0.f;
+        for (int nt = 0; nt < P::NT; ++nt)
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) z[g][nr] = 0.f;
-    }
+          for (int k = 0; k < 4; ++k) o[g][mt][nt][k] = 0.f;
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      m[nr] = -INFINITY;
-      l[nr] = 0.f;
-    }
+    for (int ns = 0; ns < P::NS; ++ns)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[ns][j] = -INFINITY;
+        l[ns][j] = 0.f;
+#pragma unroll
+        for (int g = 0; g < P::kGroups; ++g) z[g][ns][j] = 0.f;
+      }
     e = -24;
   }
 };
 
-template <int D, int MODE>
+template <int D, int MODE, int FEAT>
 __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char* st, int blk, int rows, int lane,
-                                           float (&sc)[QTile<D, MODE>::NR][8]) {
+                                           float (&sc)[Shape<D, MODE>::NS][4][2]) {
   using S = Stage<D>;
-  constexpr int kGroups = D / 64, NR = QTile<D, MODE>::NR;
+  using P = Shape<D, MODE>;
+  constexpr int kGroups = P::kGroups, NS = P::NS, NT = P::NT;
   const int gid = lane >> 2, tig = lane & 3;
-  uint32_t pr[kGroups * 8];
+  uint32_t pr[kGroups * 4];
 #pragma unroll
-  for (int i = 0; i < 2 * kGroups; ++i)
-    *reinterpret_cast<uint4*>(pr + 4 * i) = *reinterpret_cast<const uint4*>(st + S::kV + S::kCodes + tig * (32 * kGroups) + 16 * i);
-  const int r0 = blk * kRows + 8 * tig;
+  for (int i = 0; i < kGroups; ++i)
+    *reinterpret_cast<uint4*>(pr + 4 * i) = *reinterpret_cast<const uint4*>(st + S::kV + S::kCodes + gid * (16 * kGroups) + 16 * i);
   if ((blk + 1) * kRows > rows) {  // rows behind the cache's end hold anything, NaN among it
+    const int r0 = blk * kRows + 4 * gid;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r0 + i >= rows)
+    for (int i = 0; i < 4; ++i)
+      if (r0 + i >= rows) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) pr[i * kGroups + g] = 0u;
+      }
   }
-  // the largest scale (low half of each pair), for the unit of the weights below
   __half2 mx = *reinterpret_cast<const __half2*>(&pr[0]);
 #pragma unroll
-  for (int i = 1; i < 8 * kGroups; ++i) mx = __hmax2(mx, *reinterpret_cast<const __half2*>(&pr[i]));
-  mx = __hmax2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = __hmax2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  const int eb = ((*reinterpret_cast<const uint32_t*>(&mx) >> 10) & 31u) - 15;
-  float unit = 1.f;
-  const int e = min(max(eb, A.e), 15);
-  if (e != A.e) {
-    unit = pow2i(A.e - e);
+  for (int i = 1; i < 4 * kGroups; ++i) mx = __hmax2(mx, *reinterpret_cast<const __half2*>(&pr[i]));
+  const int eb = min((int)((*reinterpret_cast<const uint32_t*>(&mx) >> 10) & 31u) - 15, 15);  // of the largest scale (low halves)
+  bool over = eb > A.e;
+#pragma unroll
+  for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      over = over || fmaxf(fmaxf(sc[ns][0][j], sc[ns][1][j]), fmaxf(sc[ns][2][j], sc[ns][3][j])) > A.m[ns][j] + kSlack;
+  if (__any_sync(0xffffffffu, over)) {
+    const int e = max(A.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)(eb + 32)) - 32);
+    const float unit = pow2i(A.e - e);
     A.e = e;
+    float al[NS][2];
+#pragma unroll
+    for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float bm = fmaxf(fmaxf(sc[ns][0][j], sc[ns][1][j]), fmaxf(sc[ns][2][j], sc[ns][3][j]));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
+        const float nm = fmaxf(A.m[ns][j], bm);
+        al[ns][j] = nm == -INFINITY ? 1.f : ex2(A.m[ns][j] - nm);
+        A.m[ns][j] = nm;
+        A.l[ns][j] *= al[ns][j];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) A.z[g][ns][j] *= al[ns][j];
+        al[ns][j] *= unit;
+      }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) A.o[g][mt][nt][k] *= al[NS == 2 ? nt : 0][k & 1];
   }
-  float al[NR];
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    float bm = sc[nr][0];
+  for (int ns = 0; ns < NS; ++ns)
 #pragma unroll
-    for (int i = 1; i < 8; ++i) bm = fmaxf(bm, sc[nr][i]);
-    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-    const float nm = fmaxf(A.m[nr], bm);
-    const float base = nm == -INFINITY ? 0.f : nm;
-    al[nr] = ex2(A.m[nr] - base);
-    A.m[nr] = nm;
-    float ps = 0.f;
+    for (int j = 0; j < 2; ++j) {
+      const float base = A.m[ns][j] == -INFINITY ? 0.f : A.m[ns][j];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sc[nr][i] = ex2(sc[nr][i] - base);
-      ps += sc[nr][i];
+      for (int i = 0; i < 4; ++i) {
+        sc[ns][i][j] = ex2(sc[ns][i][j] - base);
+        A.l[ns][j] += sc[ns][i][j];
+      }
     }
-    A.l[nr] = fmaf(A.l[nr], al[nr], ps);
-  }
-  const float f = pow2i(13 - A.e);
-  const float a0 = al[0] * unit, a1 = MODE == 2 ? al[NR - 1] * unit : a0;
+  const float f = pow2i(kUnit - A.e);
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    uint32_t af[2][4];
+    uint32_t bf[NT][4];  // P^T as B fragments: register i holds rows 8 tig + i and 8 tig + 4 + i of column gid
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) A.z[g][nr] *= al[nr];
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = unpack_half(pr[i * kGroups + g]);
+      const float z = P::kPrecise ? fmaf(p.x, 7.5f, p.y) : p.y, sf = p.x * f;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {  // cache rows 8 tig + 4 kk .. + 3
-      if (MODE == 1) af[kk][1] = af[kk][3] = 0u;
+      for (int ns = 0; ns < NS; ++ns) {
+        float x[2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int i = 4 * kk + 2 * y;
-        const float2 p0 = unpack_half(pr[i * kGroups + g]), p1 = unpack_half(pr[(i + 1) * kGroups + g]);
-        const float z0 = MODE == 0 ? fmaf(p0.x, 7.5f, p0.y) : p0.y, z1 = MODE == 0 ? fmaf(p1.x, 7.5f, p1.y) : p1.y;
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          // a weight of zero (a masked row) takes nothing of its row, NaN included
-          const float w0 = sc[nr][i], w1 = sc[nr][i + 1];
-          const float x0 = w0 > 0.f ? w0 * (p0.x * f) : w0, x1 = w1 > 0.f ? w1 * (p1.x * f) : w1;
-          A.z[g][nr] += w0 > 0.f ? w0 * z0 : w0;
-          A.z[g][nr] += w1 > 0.f ? w1 * z1 : w1;
-          const uint32_t hi = pack_half(x0, x1);
-          if (MODE == 0) {
-            const float2 u = unpack_half(hi);
-            af[kk][2 * y] = hi;
-            af[kk][2 * y + 1] = pack_half(x0 - u.x, x1 - u.y);
+        for (int j = 0; j < 2; ++j) {
+          const float w = sc[ns][i][j];
+          if (FEAT == 2) {  // a weight of zero (a masked row) takes nothing of its row, NaN included
+            x[j] = w > 0.f ? w * sf : w;
+            A.z[g][ns][j] += w > 0.f ? w * z : w;
           } else {
-            af[kk][2 * y + nr] = hi;
+            x[j] = w * sf;
+            A.z[g][ns][j] = fmaf(w, z, A.z[g][ns][j]);
           }
+        }
+        const uint32_t hi = pack_half(x[0], x[1]);
+        if (P::kPrecise) {
+          const float2 u = unpack_half(hi);
+          const uint32_t lo = pack_half(x[0] - u.x, x[1] - u.y);
+          if (MODE == FP32_4) {
+            bf[0][i] = transpose8(tig < 2 ? hi : lo);
+          } else {
+            bf[0][i] = transpose8(hi);
+            bf[NT - 1][i] = transpose8(lo);
+          }
+        } else {
+          bf[ns][i] = transpose8(hi);
         }
       }
     }
     // The block's share is summed from zero and added in fp32: the tensor cores' own sums are truncated, and
     // over thousands of rows that bias showed (3e-4).  For fp32 they also start at -7.5 sum(p), so that
     // codes count from their middle: sum p (code - 7.5) is of the output's size, sum p code many times that.
-    float mid[4] = {0.f, 0.f, 0.f, 0.f};
-    if (MODE == 0) {
+    float mid[NT][4];
+    if (P::kPrecise) {
       constexpr uint32_t kMinus = 0x81e081e0u;  // -480 * 2^-24: -7.5 in units of 2^-18
-      mma_16816(mid, af[0], kMinus, kMinus);
-      mma_16816(mid, af[1], kMinus, kMinus);
+      constexpr uint32_t am[4] = {kMinus, kMinus, kMinus, kMinus};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma(mid[nt], am, bf[nt][0], bf[nt][1], 0.f, 0.f, 0.f, 0.f);
+        mma(mid[nt], am, bf[nt][2], bf[nt][3], mid[nt][0], mid[nt][1], mid[nt][2], mid[nt][3]);
+      }
     }
     const unsigned char* vb = st + S::kV + g * 1024 + 4 * gid;
     uint32_t w[8];
@@ -706,18 +812,21 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
       const uint32_t sel = half ? 0x7632u : 0x5410u;
       uint32_t x[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) codes<MODE == 0>(__byte_perm(w[2 * i], w[2 * i + 1], sel), x[i]);
+      for (int i = 0; i < 4; ++i) codes<P::kPrecise>(__byte_perm(w[i], w[i + 4], sel), x[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float c[4] = {mid[0], mid[1], mid[2], mid[3]};
-        mma_16816(c, af[0], x[0][i], x[1][i]);
-        mma_16816(c, af[1], x[2][i], x[3][i]);
-        float(&o)[4] = A.o[g][4 * half + i];
-        o[0] = fmaf(o[0], a0, c[0]);
-        o[1] = fmaf(o[1], a0, c[1]);
-        o[2] = fmaf(o[2], a1, c[2]);
-        o[3] = fmaf(o[3], a1, c[3]);
-      }
+      for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t a0[4] = {x[0][2 * m2], x[0][2 * m2 + 1], x[1][2 * m2], x[1][2 * m2 + 1]};
+          const uint32_t a1[4] = {x[2][2 * m2], x[2][2 * m2 + 1], x[3][2 * m2], x[3][2 * m2 + 1]};
+          float c[4];
+          if (P::kPrecise) mma(c, a0, bf[nt][0], bf[nt][1], mid[nt][0], mid[nt][1], mid[nt][2], mid[nt][3]);
+          else mma(c, a0, bf[nt][0], bf[nt][1], 0.f, 0.f, 0.f, 0.f);
+          mma(c, a1, bf[nt][2], bf[nt][3], c[0], c[1], c[2], c[3]);
+          float(&o)[4] = A.o[g][2 * half + m2][nt];
+          add2(o[0], o[1], c[0], c[1]);
+          add2(o[2], o[3], c[2], c[3]);
+        }
     }
   }
 }
@@ -726,59 +835,65 @@ __device__ __forceinline__ void store_out(const Kv4Attn& a, size_t at, const flo
   if (a.bf16) store8(reinterpret_cast<__nv_bfloat16*>(a.out) + at, x);
   else store8(reinterpret_cast<float*>(a.out) + at, x);
 }
-
-// The end of a tile's run: the sums over the row's four lanes; then either the output itself or the
-// partial (o [d], m, l) of each row at `dep` (rows d + 2 floats apart).
-template <int D, int MODE>
-__device__ __forceinline__ void finish(Acc<D, MODE>& A, const AttnArgs& a, const SeqInfo& sq, int h, int tile, int lane, float* dep) {
-  constexpr int kGroups = D / 64, NR = QTile<D, MODE>::NR, TILE = 8 * NR;
-  const int gid = lane >> 2, tig = lane & 3;
-  const float unit = pow2i(A.e - 13 + 24);
+__device__ __forceinline__ float all_rows(float x) {  // sum over the lanes of a column
 #pragma unroll
-  for (int nr = 0; nr < NR; ++nr) {
-    float l = A.l[nr];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const int row = tile * TILE + gid + 8 * nr, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
-    const bool on = tok < sq.c;
-    const float inv = dep != nullptr ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      float z = A.z[g][nr];
-      z += __shfl_xor_sync(0xffffffffu, z, 1);
-      z += __shfl_xor_sync(0xffffffffu, z, 2);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float o = MODE == 0 ? A.o[g][j][c] + A.o[g][j][2 + c] : A.o[g][j][2 * nr + c];
-          x[j] = fmaf(o, MODE == 0 ? unit / 64.f : (j & 1) ? unit / 16.f : unit, z) * inv;
-        }
-        if (!on) continue;
-        if (dep != nullptr) {
-          float* d = dep + (gid + 8 * nr) * (D + 2) + 64 * g + 16 * tig + 8 * c;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = x[j];
-        } else {
-          store_out(a.a, (size_t)(sq.tok0 + tok) * a.a.ldo + (size_t)head * D + 64 * g + 16 * tig + 8 * c, x);
-        }
-      }
-    }
-    if (on && tig == 0) {
-      if (dep != nullptr) {
-        dep[(gid + 8 * nr) * (D + 2) + D] = A.m[nr];
-        dep[(gid + 8 * nr) * (D + 2) + D + 1] = l;
-      } else if (a.lse != nullptr) {
-        a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = l > 0.f ? A.m[nr] + log2f(l) : INFINITY;
-      }
-    }
-  }
+  for (int m = 4; m < 32; m <<= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  return x;
 }
 
-template <int D, int MODE, bool EXTRA>
+// The end of a tile's run: the sums over the columns' lanes; then either the output itself or the
+// partial (o [d], m, l) of each column at `dep` (d + 2 floats apart).
+template <int D, int MODE>
+__device__ __forceinline__ void finish(Acc<D, MODE>& A, const AttnArgs& a, const SeqInfo& sq, int h, int tile, int lane, float* dep) {
+  using P = Shape<D, MODE>;
+  constexpr int NS = P::NS;
+  const int gid = lane >> 2, tig = lane & 3;
+  const float unit = pow2i(A.e - kUnit + 24);
+  const float u0 = P::kPrecise ? unit / 64.f : unit, u1 = P::kPrecise ? u0 : unit / 16.f;
+#pragma unroll
+  for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float l = all_rows(A.l[ns][j]);
+      const int col = column<MODE>(tig, ns, j), row = tile * P::TILE + col, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
+      const bool on = tok < sq.c && !(MODE == FP32_4 && tig >= 2);
+      const float inv = dep != nullptr ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
+#pragma unroll
+      for (int g = 0; g < P::kGroups; ++g) {
+        const float z = all_rows(A.z[g][ns][j]);
+        float x[8];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float o = A.o[g][mt][NS == 2 ? ns : 0][2 * y + j];
+            if (MODE == FP32_8) o += A.o[g][mt][P::NT - 1][2 * y + j];
+            if (MODE == FP32_4) o += __shfl_xor_sync(0xffffffffu, o, 2);
+            x[2 * mt + y] = fmaf(o, y ? u1 : u0, z) * inv;
+          }
+        if (!on) continue;
+        if (dep != nullptr) {
+          float* d = dep + col * (D + 2) + 64 * g + 8 * gid;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = x[i];
+        } else {
+          store_out(a.a, (size_t)(sq.tok0 + tok) * a.a.ldo + (size_t)head * D + 64 * g + 8 * gid, x);
+        }
+      }
+      if (on && gid == 0) {
+        if (dep != nullptr) {
+          dep[col * (D + 2) + D] = A.m[ns][j];
+          dep[col * (D + 2) + D + 1] = l;
+        } else if (a.lse != nullptr) {
+          a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = l > 0.f ? A.m[ns][j] + log2f(l) : INFINITY;
+        }
+      }
+    }
+}
+
+template <int D, int MODE, int FEAT>
 __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int TILE = QTile<D, MODE>::TILE, kWarps = Shape<D, MODE>::kWarps, kStages = Shape<D, MODE>::kStages;
+  constexpr int TILE = Shape<D, MODE>::TILE, kWarps = Shape<D, MODE>::kWarps, kStages = Shape<D, MODE>::kStages;
   static_assert(kStages * Stage<D>::kBytes >= TILE * (D + 2) * 4, "a warp's last partial lies in its ring");
   using S = Stage<D>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -803,7 +918,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
   const uint32_t mine_s = smem_of(mine);
 
   if (u0 < u1) {
-    const bool need_pos = EXTRA && a.g.track;
+    const bool need_pos = FEAT > 0 && a.g.track;
     Seg ps = locate(sp, u0);  // the copies' segment
     Seg cs = ps;              // the arithmetic's
     SeqInfo psq = info[ps.s], csq = psq;
@@ -843,7 +958,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
         cs = locate(sp, u);
         csq = info[cs.s];
       }
-      load_q<D, MODE>(qt, a, csq, cs.s, cs.h, cs.tile, lane);
+      load_q<D, MODE, FEAT>(qt, a, csq, cs.s, cs.h, cs.tile, lane);
       acc.clear();
       const int first_limit = csq.r - csq.c + (cs.tile * TILE) / a.grp;
       const int end = min(u1, cs.u0 + cs.n);
@@ -855,9 +970,9 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
         issue(u + kStages - 1);  // into the stage that the iteration before has read
         if (use) {
           const unsigned char* st = mine + stg * S::kBytes;
-          float sc[QTile<D, MODE>::NR][8];
-          scores<D, MODE, EXTRA>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first_limit, lane, sc);
-          accumulate<D, MODE>(acc, st, blk, csq.r, lane, sc);
+          float sc[Shape<D, MODE>::NS][4][2];
+          scores<D, MODE, FEAT>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first_limit, lane, sc);
+          accumulate<D, MODE, FEAT>(acc, st, blk, csq.r, lane, sc);
         }
         __syncwarp();
       }
@@ -965,10 +1080,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 // of exp2(score - lse).  A warp owns a block's 32 rows and goes through all the query tiles, so the
 // sums have one order and no atomics; the scores are computed again from K (half a row's bytes)
 // rather than kept, which would cost 4 bytes written and read for each of the group's heads.
-template <int D, int MODE, bool EXTRA>
+template <int D, int MODE, int FEAT>
 __global__ void __launch_bounds__(256) weight_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int TILE = QTile<D, MODE>::TILE, NR = QTile<D, MODE>::NR;
+  using P = Shape<D, MODE>;
   using S = Stage<D>;
+  constexpr int TILE = P::TILE;
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int s = blockIdx.z, h = blockIdx.y;
@@ -980,43 +1096,39 @@ __global__ void __launch_bounds__(256) weight_kernel(const __grid_constant__ Att
   for (int blk = blockIdx.x * 8 + warp; blk < nblk; blk += gridDim.x * 8) {
     uint8_t* p = block_of(a.g, a.b.tables + (size_t)s * a.g.max_pages, a.layer, h, blk * kRows, nullptr);
     if (p == nullptr) continue;
-    fetch<D>(smem_of(st), p, EXTRA, lane);
+    fetch<D>(smem_of(st), p, FEAT > 0, lane);
     cp_commit();
     cp_wait<0>();
     __syncwarp();
-    float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 0.f;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
     for (int tile = 0; tile < tiles; ++tile) {
       const int last = v.r - v.c + min(v.c - 1, (tile * TILE + TILE - 1) / a.grp), first = v.r - v.c + tile * TILE / a.grp;
       if (blk * kRows > last) continue;
       QTile<D, MODE> qt;
-      load_q<D, MODE>(qt, a, sq, s, h, tile, lane);
-      float sc[NR][8];
-      scores<D, MODE, EXTRA>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first, lane, sc);
+      load_q<D, MODE, FEAT>(qt, a, sq, s, h, tile, lane);
+      float sc[P::NS][4][2];
+      scores<D, MODE, FEAT>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first, lane, sc);
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        const int row = tile * TILE + gid + 8 * nr, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
-        const float lse = tok < v.c ? a.lse[(size_t)(v.tok0 + tok) * a.g.nq + head] : INFINITY;
+      for (int ns = 0; ns < P::NS; ++ns)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] += tok < v.c ? ex2(sc[nr][i] - lse) : 0.f;
-      }
-    }
+        for (int j = 0; j < 2; ++j) {
+          const int row = tile * TILE + column<MODE>(tig, ns, j), tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
+          if (tok >= v.c || (MODE == FP32_4 && tig >= 2)) continue;
+          const float lse = a.lse[(size_t)(v.tok0 + tok) * a.g.nq + head];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 4);
-      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 8);
-      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 16);
-    }
-    if (gid == 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 8 * tig + i;
-        if (blk * kRows + r < v.r) {
-          float* at = reinterpret_cast<float*>(p + weight_at(D)) + r;
-          *at += w[i];
+          for (int i = 0; i < 4; ++i) w[i] += ex2(sc[ns][i][j] - lse);
         }
-      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
+      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
+    }
+    if (tig == 0) {
+      float* at = reinterpret_cast<float*>(p + weight_at(D)) + 4 * gid;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (blk * kRows + 4 * gid + i < v.r) at[i] += w[i];
     }
     __syncwarp();
   }
@@ -1248,45 +1360,50 @@ cudaError_t launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaSt
   return cudaLaunchKernelEx(&c, fn, args...);
 }
 
-int tile_of(const Kv4Geom& g, const Kv4Batch& b, int bf16) { return bf16 && b.max_count * (g.nq / g.nkv) > 8 ? 16 : 8; }
-
 // Units of the batch at most.
 long long max_units(const Kv4Geom& g, const Kv4Batch& b, int tile) {
   const long long tiles = ((long long)b.max_count * (g.nq / g.nkv) + tile - 1) / tile;
   return (long long)b.n_seq * g.nkv * tiles * std::max(1, (b.max_rows + kRows - 1) / kRows);
 }
 
-template <int D, int MODE, bool EXTRA>
+template <int D, int MODE, int FEAT>
 cudaError_t run_attention(AttnArgs a, int num_sms, cudaStream_t st) {
-  constexpr int TILE = MODE == 2 ? 16 : 8, kWarps = Shape<D, MODE>::kWarps, kStages = Shape<D, MODE>::kStages;
+  constexpr int TILE = Shape<D, MODE>::TILE, kWarps = Shape<D, MODE>::kWarps, kStages = Shape<D, MODE>::kStages;
   a.warps = kWarps;
   using S = Stage<D>;
   static std::once_flag once[64], once_w[64];
   const size_t info = ((size_t)a.b.n_seq * sizeof(SeqInfo) + 127) / 128 * 128;
   const int dep_rows = std::min<long long>(TILE, (long long)a.b.max_count * a.grp);
   const size_t smem = info + (size_t)kWarps * kStages * S::kBytes + (size_t)kWarps * dep_rows * (D + 2) * 4;
-  if (cudaError_t e = allow_smem((const void*)attn_kernel<D, MODE, EXTRA>, once, kAttnSmem)) return e;
+  if (cudaError_t e = allow_smem((const void*)attn_kernel<D, MODE, FEAT>, once, kAttnSmem)) return e;
   const long long units = max_units(a.g, a.b, TILE);
   const int grid = (int)std::max<long long>(1, std::min<long long>(num_sms, (units + kWarps - 1) / kWarps));
-  if (cudaError_t e = launch(attn_kernel<D, MODE, EXTRA>, dim3(grid), kWarps * 32, smem, st, false, a)) return e;
+  if (cudaError_t e = launch(attn_kernel<D, MODE, FEAT>, dim3(grid), kWarps * 32, smem, st, false, a)) return e;
   if (grid > 1) {
     const long long segs = (long long)a.g.nkv * (((long long)a.b.max_count * a.grp + TILE - 1) / TILE);
     if (cudaError_t e = launch(combine_kernel<D, TILE>, dim3((unsigned)std::min<long long>(segs, 4096), a.b.n_seq), 256, info, st, true, a)) return e;
   }
   if (a.lse != nullptr) {
-    if (cudaError_t e = allow_smem((const void*)weight_kernel<D, MODE, EXTRA>, once_w, kAttnSmem)) return e;
+    if (cudaError_t e = allow_smem((const void*)weight_kernel<D, MODE, FEAT>, once_w, kAttnSmem)) return e;
     const int bx = std::max(1, std::min(1024, (a.b.max_rows + 8 * kRows - 1) / (8 * kRows)));
-    return launch(weight_kernel<D, MODE, EXTRA>, dim3(bx, a.g.nkv, a.b.n_seq), 256, (size_t)8 * S::kBytes, st, false, a);
+    return launch(weight_kernel<D, MODE, FEAT>, dim3(bx, a.g.nkv, a.b.n_seq), 256, (size_t)8 * S::kBytes, st, false, a);
   }
   return cudaSuccess;
 }
 
+template <int D, int MODE>
+cudaError_t pick_feat(const AttnArgs& a, int num_sms, cudaStream_t st) {
+  if (a.b.max_count > 1 || a.a.window > 0) return run_attention<D, MODE, 2>(a, num_sms, st);
+  if (a.a.cap > 0.f || a.a.slopes != nullptr) return run_attention<D, MODE, 1>(a, num_sms, st);
+  return run_attention<D, MODE, 0>(a, num_sms, st);
+}
+
+// The narrowest tile that holds a sequence's queries of one KV head, or else the widest.
 template <int D>
 cudaError_t pick_attention(const AttnArgs& a, int num_sms, cudaStream_t st) {
-  const bool extra = a.a.cap > 0.f || a.a.slopes != nullptr || a.a.window > 0;
-  if (!a.a.bf16) return extra ? run_attention<D, 0, true>(a, num_sms, st) : run_attention<D, 0, false>(a, num_sms, st);
-  if (tile_of(a.g, a.b, 1) == 8) return extra ? run_attention<D, 1, true>(a, num_sms, st) : run_attention<D, 1, false>(a, num_sms, st);
-  return extra ? run_attention<D, 2, true>(a, num_sms, st) : run_attention<D, 2, false>(a, num_sms, st);
+  const long long cols = (long long)a.b.max_count * a.grp;
+  if (a.a.bf16) return cols <= 8 ? pick_feat<D, BF16_8>(a, num_sms, st) : pick_feat<D, BF16_16>(a, num_sms, st);
+  return cols <= 4 ? pick_feat<D, FP32_4>(a, num_sms, st) : pick_feat<D, FP32_8>(a, num_sms, st);
 }
 
 // Tokens of a CTA of append and read: about 2,048 vectors of 8.
@@ -1338,6 +1455,7 @@ cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const 
   a.layer = layer;
   a.grp = g.nq / g.nkv;
   a.grid_max = num_sms;
+  a.cap2 = at.cap > 0.f ? 2.f * kLog2e / at.cap : 0.f;
   a.part = reinterpret_cast<float*>(ws);
   a.lse = at.accumulate ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256((size_t)num_sms * 2 * 16 * (g.d + 2) * 4)) : nullptr;
   return g.d == 64 ? pick_attention<64>(a, num_sms, st) : pick_attention<128>(a, num_sms, st);
