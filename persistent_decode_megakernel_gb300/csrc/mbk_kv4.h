@@ -1,4 +1,5 @@
-// mbk_kv4.h -- the 4-bit KV cache's pool, batches and launches (mbk_kv4.cu), used by the C ABI
+// mbk_kv4.h -- the 4-bit KV cache's pool, batches and launches (mbk_kv4_attn.cu,
+// mbk_kv4_rows.cu), used by the C ABI
 // (mbk_kv4_api.cu) and by the prefill path of a handle whose pool is held in 4 bits.
 #pragma once
 #include <cuda_runtime.h>
