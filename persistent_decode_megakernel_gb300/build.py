@@ -20,10 +20,11 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmbk.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
-CU_SOURCES = ["mbk_kernel.cu", "mbk_api.cu", "mbk_static.cu", "mbk_prefill.cu", "mbk_kv4_attn.cu", "mbk_kv4_rows.cu",
-              "mbk_kv4_api.cu"]
+CU_SOURCES = ["mbk_kernel.cu", "mbk_api.cu", "mbk_static.cu", "mbk_prefill.cu", "mbk_kv4_attn.cu", "mbk_kv4_prompt.cu",
+              "mbk_kv4_rows.cu", "mbk_kv4_api.cu"]
 CPP_SOURCES = ["mbk_sched.cpp", "mbk_simulate.cpp", "mbk_args.cpp"]
-HEADERS = ["mbk_plan.h", "mbk_device.h", "mbk_sched.h", "mbk_prefill.h", "mbk_args.h", "mbk_kv4.h", "mbk_kv4_device.h"]
+HEADERS = ["mbk_plan.h", "mbk_device.h", "mbk_sched.h", "mbk_prefill.h", "mbk_args.h", "mbk_kv4.h", "mbk_kv4_device.h",
+           "mbk_kv4_split.h"]
 
 
 def _cuda_home() -> str:

@@ -24,6 +24,7 @@
 // hi + lo fp16 (22 bits), the softmax weights likewise; up to 4 queries hold hi in columns 0 .. 3 and lo
 // in 4 .. 7, so that one mma does both, more take a second tile.  bf16 queries need one fp16 each.
 #include "mbk_kv4_device.h"
+#include "mbk_kv4_split.h"
 
 namespace mbk {
 namespace {
@@ -59,15 +60,12 @@ struct Shape {
 // per warp, whatever the sequences' lengths: a long context is spread over all SMs and a batch of
 // short ones leaves none idle.  A segment inside one warp's run is written by the warp, one inside a
 // CTA's run is joined in shared memory, the rest is joined by combine_kernel.
-struct SeqInfo {
-  int cum, r, c, tok0;  // units before the sequence; rows, new tokens, first token
-};
-
 struct AttnArgs {
   Kv4Geom g;
   Kv4Batch b;
   Kv4Attn a;
   int layer, grp, grid_max, warps;
+  int below;     // query rows per KV head from which on a sequence is the prompt kernel's, or 0
   float scale2, cap_in, cap_out;  // scale log2(e); 2 / cap, cap log2(e)
   float* part;   // [grid][2][tile columns][d + 4] partial (o, m, l) of segments that several CTAs share
   float* lse;    // [n_tokens][nq] log2 of the softmax denominators (accumulate), or null
@@ -103,7 +101,6 @@ __device__ Split<TILE> make_split(const AttnArgs& a, SeqInfo* info, int* warp_su
   sp.window = a.a.window;
   sp.track = a.g.track;
   sp.seq = info;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   int carry = 0;
   for (int s0 = 0; s0 < a.b.n_seq; s0 += blockDim.x) {
     const int s = s0 + threadIdx.x;
@@ -112,28 +109,16 @@ __device__ Split<TILE> make_split(const AttnArgs& a, SeqInfo* info, int* warp_su
     if (s < a.b.n_seq) {
       const SeqView v = seq_view(a.g, a.b, s, report);
       q.r = v.r;
-      q.c = v.c;
+      q.c = a.below == 0 || v.c * a.grp < a.below ? v.c : 0;  // longer ones are the prompt kernel's
       q.tok0 = v.tok0;
       n = sp.units(q);
     }
-    int x = n;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, m);
-      if (lane >= m) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int before = carry, all = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += warp_sums[w];
-      all += warp_sums[w];
-    }
-    q.cum = before + x - n;
+    int total;
+    q.cum = carry + block_scan(n, warp_sums, &total);
     if (s < a.b.n_seq) info[s] = q;
-    carry += all;
-    __syncthreads();
+    carry += total;
   }
+  __syncthreads();
   sp.total = carry;
   // one block for each warp of a CTA before a second CTA is used
   sp.grid = max(1, min(a.grid_max, (carry + a.warps - 1) / a.warps));
@@ -589,10 +574,6 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
   }
 }
 
-__device__ __forceinline__ void store_out(const Kv4Attn& a, size_t at, const float (&x)[8]) {
-  if (a.bf16) store8(reinterpret_cast<__nv_bfloat16*>(a.out) + at, x);
-  else store8(reinterpret_cast<float*>(a.out) + at, x);
-}
 __device__ __forceinline__ float all_rows(float x) {  // sum over the lanes of a column
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
@@ -645,53 +626,6 @@ __device__ __forceinline__ void finish(Acc<D, MODE>& A, const AttnArgs& a, const
         }
       }
     }
-}
-
-// Joins n partials of a segment of `cols` columns, at(k) being the k-th's place, and writes the output (and
-// lse), or with `to` the joined partial.  2^x threads take the partials of 8 dims of a column between them.  All
-// threads of the CTA call.
-template <int D, typename At>
-__device__ __forceinline__ void join(const AttnArgs& a, const SeqInfo& sq, int h, int row0, int cols, int n, float* to, At at) {
-  constexpr int kPart = D + 4;
-  const int items = cols * (D / 8);
-  int sl = 32;
-  while (sl > 1 && (sl >= 2 * n || items * sl > (int)blockDim.x)) sl >>= 1;
-  for (int x = threadIdx.x; x < (items * sl + 31) / 32 * 32; x += blockDim.x) {
-    const int item = min(x / sl, items - 1), k0 = x % sl, col = item / (D / 8), d0 = item % (D / 8) * 8;
-    float m = -INFINITY;
-    for (int k = k0; k < n; k += sl) m = fmaxf(m, at(k)[col * kPart + D]);
-    for (int i = 1; i < sl; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = k0; k < n; k += sl) {
-      const float* p = at(k) + col * kPart;
-      const float w = ex2(p[D] - base);
-      const float4 u = *reinterpret_cast<const float4*>(p + d0), v = *reinterpret_cast<const float4*>(p + d0 + 4);
-      l = fmaf(p[D + 1], w, l);
-      o[0] = fmaf(u.x, w, o[0]), o[1] = fmaf(u.y, w, o[1]), o[2] = fmaf(u.z, w, o[2]), o[3] = fmaf(u.w, w, o[3]);
-      o[4] = fmaf(v.x, w, o[4]), o[5] = fmaf(v.y, w, o[5]), o[6] = fmaf(v.z, w, o[6]), o[7] = fmaf(v.w, w, o[7]);
-    }
-    for (int i = 1; i < sl; i <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], i);
-    }
-    if (k0 != 0 || x / sl >= items) continue;
-    if (to != nullptr) {
-      store8(to + col * kPart + d0, o);
-      if (d0 == 0) {
-        to[col * kPart + D] = m;
-        to[col * kPart + D + 1] = l;
-      }
-    } else {
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] *= inv;
-      const int row = row0 + col, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
-      store_out(a.a, (size_t)(sq.tok0 + tok) * a.a.ldo + (size_t)head * D + d0, o);
-      if (a.lse != nullptr && d0 == 0) a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = l > 0.f ? m + log2f(l) : INFINITY;
-    }
-  }
 }
 
 template <int D, int MODE, int FEAT>
@@ -939,7 +873,7 @@ long long max_units(const Kv4Geom& g, const Kv4Batch& b, int tile) {
 }
 
 template <int D, int MODE, int FEAT>
-cudaError_t run_attention(AttnArgs a, int num_sms, cudaStream_t st) {
+cudaError_t run_attention(AttnArgs a, bool others, int num_sms, cudaStream_t st) {
   constexpr int TILE = Shape<D, MODE>::TILE, kWarps = Shape<D, MODE>::kWarps, kStages = Shape<D, MODE>::kStages;
   a.warps = kWarps;
   using S = Stage<D>;
@@ -950,14 +884,16 @@ cudaError_t run_attention(AttnArgs a, int num_sms, cudaStream_t st) {
   if (cudaError_t e = allow_smem((const void*)attn_kernel<D, MODE, FEAT>, once, kAttnSmem)) return e;
   const long long units = max_units(a.g, a.b, TILE);
   const int grid = (int)std::max<long long>(1, std::min<long long>(num_sms, (units + kWarps - 1) / kWarps));
-  if (cudaError_t e = launch(attn_kernel<D, MODE, FEAT>, dim3(grid), kWarps * 32, smem, st, false, a)) return e;
-  if (grid > 1) {
+  if (others)
+    if (cudaError_t e = launch(attn_kernel<D, MODE, FEAT>, dim3(grid), kWarps * 32, smem, st, false, a)) return e;
+  if (others && grid > 1) {
     const long long segs = (long long)a.g.nkv * (((long long)a.b.max_count * a.grp + TILE - 1) / TILE);
     if (cudaError_t e = launch(combine_kernel<D, TILE>, dim3((unsigned)std::min<long long>(segs, 4096), a.b.n_seq), 512, info, st, true, a)) return e;
   }
   if (a.lse != nullptr) {
     if (cudaError_t e = allow_smem((const void*)weight_kernel<D, MODE, FEAT>, once_w, kAttnSmem)) return e;
     a.warps = kWeightWarps;
+    a.below = 0;  // every sequence's rows
     a.grid_max = 2 * num_sms;
     const long long blocks = (long long)a.b.n_seq * a.g.nkv * std::max(1, (a.b.max_rows + kRows - 1) / kRows);
     const int wg = (int)std::max<long long>(1, std::min<long long>(a.grid_max, (blocks + kWeightWarps - 1) / kWeightWarps));
@@ -967,24 +903,37 @@ cudaError_t run_attention(AttnArgs a, int num_sms, cudaStream_t st) {
 }
 
 template <int D, int MODE>
-cudaError_t pick_feat(const AttnArgs& a, int num_sms, cudaStream_t st) {
-  if (a.b.max_count > 1 || a.a.window > 0) return run_attention<D, MODE, 2>(a, num_sms, st);
-  if (a.a.cap > 0.f || a.a.slopes != nullptr) return run_attention<D, MODE, 1>(a, num_sms, st);
-  return run_attention<D, MODE, 0>(a, num_sms, st);
+cudaError_t pick_feat(const AttnArgs& a, bool others, int num_sms, cudaStream_t st) {
+  if (a.b.max_count > 1 || a.a.window > 0) return run_attention<D, MODE, 2>(a, others, num_sms, st);
+  if (a.a.cap > 0.f || a.a.slopes != nullptr) return run_attention<D, MODE, 1>(a, others, num_sms, st);
+  return run_attention<D, MODE, 0>(a, others, num_sms, st);
 }
 
 // The narrowest tile that holds a sequence's queries of one KV head, or else the widest.
 template <int D>
-cudaError_t pick_attention(const AttnArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t pick_attention(const AttnArgs& a, bool others, int num_sms, cudaStream_t st) {
   const long long cols = (long long)a.b.max_count * a.grp;
-  if (a.a.bf16) return cols <= 8 ? pick_feat<D, BF16_8>(a, num_sms, st) : pick_feat<D, BF16_16>(a, num_sms, st);
-  return cols <= 4 ? pick_feat<D, FP32_4>(a, num_sms, st) : pick_feat<D, FP32_8>(a, num_sms, st);
+  if (a.a.bf16) return cols <= 8 ? pick_feat<D, BF16_8>(a, others, num_sms, st) : pick_feat<D, BF16_16>(a, others, num_sms, st);
+  return cols <= 4 ? pick_feat<D, FP32_4>(a, others, num_sms, st) : pick_feat<D, FP32_8>(a, others, num_sms, st);
+}
+
+// Query rows per KV head from which on a sequence goes to the prompt kernel.
+constexpr int kPromptRows = 33;
+
+// Whether the batch may have a sequence for the prompt kernel (fp32 at head dim 128 would need two accumulators and
+// operands twice as large per tile: the decode kernel takes it).
+bool has_prompts(const Kv4Geom& g, const Kv4Batch& b, int bf16) {
+  return (long long)b.max_count * (g.nq / g.nkv) >= kPromptRows && (bf16 || g.d == 64);
+}
+size_t part_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
+  const size_t own = round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
+  return own + ((long long)b.max_count * (g.nq / g.nkv) >= kPromptRows ? round256(kv4_prompt_partials(g, b, num_sms)) : 0);
 }
 
 }  // namespace
 
 size_t kv4_attention_workspace(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
-  return round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4) + round256((size_t)b.n_tokens * g.nq * 4);
+  return part_bytes(g, b, num_sms) + (g.track ? round256((size_t)b.n_tokens * g.nq * 4) : 0);
 }
 
 cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4Attn& at, void* ws, int num_sms, cudaStream_t st) {
@@ -999,8 +948,17 @@ cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const 
   a.cap_in = at.cap > 0.f ? 2.f / at.cap : 0.f;
   a.cap_out = at.cap * kLog2e;
   a.part = reinterpret_cast<float*>(ws);
-  a.lse = at.accumulate ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4)) : nullptr;
-  return g.d == 64 ? pick_attention<64>(a, num_sms, st) : pick_attention<128>(a, num_sms, st);
+  a.lse = at.accumulate ? reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + part_bytes(g, b, num_sms)) : nullptr;
+  a.below = 0;
+  const bool prompts = has_prompts(g, b, at.bf16);
+  if (prompts) {
+    // a sequence alone goes to the prompt kernel however few its tokens turn out to be
+    a.below = b.n_seq == 1 ? 1 : kPromptRows;
+    uint8_t* part = reinterpret_cast<uint8_t*>(ws) + round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
+    if (cudaError_t e = kv4_prompt(g, layer, b, at, a.below, reinterpret_cast<float*>(part), a.lse, num_sms, st)) return e;
+  }
+  const bool others = !prompts || b.n_seq > 1;
+  return g.d == 64 ? pick_attention<64>(a, others, num_sms, st) : pick_attention<128>(a, others, num_sms, st);
 }
 
 }  // namespace mbk

@@ -1,0 +1,880 @@
+// mbk_kv4_prompt.cu -- attention of many query rows (prompts, chunks of prompts) over the 4-bit KV cache, on
+// tcgen05.
+//
+// A CTA takes 128 query rows -- (token, query head) pairs that read one KV head -- through a run of key tiles
+// of 64 cache rows.  Warps 4 .. 7 turn the rows into fp16 operands in shared memory (128-byte swizzle, K as
+// [row][dim], V as [dim][row]), a lane of warp 4 issues the matrix instructions in between (a warp of its own would
+// cost all the others 32 registers), and thread i of warps 0 .. 3 owns query row i: it reads the row's scores from tensor memory, keeps its softmax and writes its
+// weights as the second product's operand.  Scores have two buffers in tensor memory and K two stages, so that the
+// tensor cores and the conversion work one tile ahead of the softmax; two CTAs share an SM, so that one's softmax
+// fills the other's waits (for which head dim 128 leaves V one stage).
+//   bf16: K and V are the values lo + scale * code rounded to fp16 (one rounding, 2^-11; bf16 has 2^-8),
+// the weights are rounded to fp16 too.
+//   fp32 (head dim 64): the operands are code - 8, exact; q and the weights are hi + lo fp16 (22 bits); the
+// softmax applies the rows' scale and lo, as the decode kernel does.  The tensor cores' sums are truncated, so the
+// output is moved to a second buffer and added there in fp32 every 8 tiles.
+//   Bound by the softmax: 64 exponentials and about 6 (fp32: 13) instructions each per row and tile.
+#include "mbk_kv4_device.h"
+#include "mbk_kv4_split.h"
+
+namespace mbk {
+namespace {
+
+constexpr int kQ = 128;        // query rows of a tile: tensor-memory lanes
+constexpr int kKeys = 64;      // cache rows of a key tile: one 128-byte row of fp16
+constexpr int kThreads = 256;  // softmax 128, conversion 128
+constexpr int kTmemCols = 256; // scores 2 x 64, output 64 or 128, fp32: sums 64
+constexpr int kFlush = 8;      // fp32: tiles between two moves of the output
+constexpr int kNotes = 4;      // tiles whose notes and pairs are kept
+constexpr float kSlack = 8.f;  // a running maximum is renewed when a score exceeds it by 2^8
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// tcgen05.mma kind::f16: fp32 sums (bits 4-5 = 1), both operands fp16 (bits 7-12 = 0) and K-major,
+// N / 8 in bits 17-22, M / 16 in bits 24-28.
+__device__ constexpr uint32_t idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kQ >> 4) << 24); }
+
+__device__ __forceinline__ void mbar_init(uint64_t* b, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* b, unsigned parity) {
+  unsigned ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_of(b)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// Waits for the phase of the given parity; false after kWaitNs, or once another thread has given up.
+__device__ __noinline__ bool mbar_wait_slow(uint64_t* b, unsigned parity, volatile unsigned* failed) {
+  unsigned long long t0 = 0ull;
+  for (unsigned spins = 0;; ++spins) {
+    if (mbar_test(b, parity)) return true;
+    if ((spins & 63u) == 63u) {
+      if (*failed != 0u) return false;
+      unsigned long long t;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t0 == 0ull) t0 = t;
+      else if (t - t0 > kWaitNs) {
+        *failed = 1u;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, unsigned parity, volatile unsigned* failed) {
+  return mbar_test(b, parity) || mbar_wait_slow(b, parity, failed);
+}
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, unsigned parity, volatile unsigned* failed) {
+  return __all_sync(0xffffffffu, mbar_wait(b, parity, failed));
+}
+
+// A K-major operand tile with the 128-byte swizzle: rows of 64 fp16 (128 bytes), 8 rows a group of 1024
+// bytes; a step of 16 along K moves the start by 32 bytes.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a),
+               "l"(b), "r"(desc), "r"(accumulate)
+               : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])),
+      "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])),
+      "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
+      "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The shared memory of a CTA.
+template <int D, bool FP32>
+struct Layout {
+  static constexpr int kGroups = D / 64, kHalves = FP32 ? 2 : 1;
+  static constexpr int kQBytes = kQ * 128 * kGroups * kHalves;  // per half and group: [128][64] fp16
+  static constexpr int kPBytes = kQ * 128 * kHalves;
+  static constexpr int kTile = kKeys * 128 * kGroups;           // K: per group [64 rows][64 dims]; V: [D dims][64 rows]
+  static constexpr int kVStages = D == 64 ? 2 : 1;
+  static constexpr int kQAt = 0, kPAt = kQBytes, kKAt = kPAt + kPBytes, kVAt = kKAt + 2 * kTile;
+  static constexpr int kPairsAt = kVAt + kVStages * kTile;      // fp32: float4 (sk, zk, sv, zv) [kNotes][64]
+  static constexpr int kPosAt = kPairsAt + (FP32 ? kNotes * kKeys * 16 : 0);
+  static constexpr int kInfoAt = kPosAt + kNotes * kKeys * 4;   // then SeqInfo [n_seq]
+};
+
+// What the conversion tells the softmax about a tile.  Written with K, at most two tiles ahead of the scores, which are
+// one ahead of the softmax: four slots.
+struct TileNote {
+  unsigned bad;                // bit b: block b of the tile lies in a page outside the pool
+  int e;                       // fp32: exponent of the largest scale of V so far
+  unsigned long long nan[2];   // bf16: rows whose V is NaN, per group of 64 dims (the operand has zeros there)
+};
+
+// ---------------------------------------------------------------- work items
+// An item is (sequence, KV head, 128 query rows, run of at most kt key tiles).  Items go round the CTAs, the
+// tiles with most keys first.
+struct Work {
+  int n_seq, nkv, grp, window, track, kt, total;
+  const SeqInfo* seq;
+  __device__ int tiles(const SeqInfo& q) const { return (q.c * grp + kQ - 1) / kQ; }
+  __device__ int first_of(const SeqInfo& q, int tile) const {
+    return window > 0 && !track ? max(0, q.r - q.c + tile * kQ / grp - window + 1) / kKeys : 0;
+  }
+  __device__ int end_of(const SeqInfo& q, int tile) const {  // key tiles [first, end) of a query tile
+    const int last = q.r - q.c + min(q.c - 1, (tile * kQ + kQ - 1) / grp);
+    return last < 0 ? 0 : last / kKeys + 1;
+  }
+  __device__ int span(const SeqInfo& q) const {  // key tiles of a query tile at most
+    int n = max(1, (q.r + kKeys - 1) / kKeys);
+    if (window > 0 && !track) n = min(n, (window + kQ / grp + 1) / kKeys + 2);
+    return n;
+  }
+  __device__ int splits(const SeqInfo& q) const { return (span(q) + kt - 1) / kt; }
+  __device__ int parts(const SeqInfo& q, int tile) const {  // the splits of a query tile that have keys
+    return (max(0, end_of(q, tile) - first_of(q, tile)) + kt - 1) / kt;
+  }
+};
+struct Item {
+  int s, h, tile, split, k0, k1, parts;
+};
+__device__ __forceinline__ Item item_at(const Work& w, int i) {
+  int lo = 0, hi = w.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (w.seq[mid].cum <= i) lo = mid; else hi = mid - 1;
+  }
+  const SeqInfo q = w.seq[lo];
+  Item it;
+  it.s = lo;
+  int rem = i - q.cum;
+  it.h = rem % w.nkv;
+  rem /= w.nkv;
+  const int ns = w.splits(q);
+  it.split = rem % ns;
+  it.tile = w.tiles(q) - 1 - rem / ns;
+  it.parts = w.parts(q, it.tile);
+  it.k0 = w.first_of(q, it.tile) + it.split * w.kt;
+  it.k1 = min(it.k0 + w.kt, w.end_of(q, it.tile));
+  return it;
+}
+
+// Fills info and returns the work; all threads call.  Two passes: units first, to choose the runs' length, then items.
+__device__ Work make_work(const PromptArgs& a, SeqInfo* info, int* sums, bool report) {
+  Work w;
+  w.n_seq = a.b.n_seq;
+  w.nkv = a.g.nkv;
+  w.grp = a.grp;
+  w.window = a.a.window;
+  w.track = a.g.track;
+  w.seq = info;
+  w.kt = 1 << 28;
+  long long units = 0, segs = 0;
+  int carry = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    carry = 0;
+    for (int s0 = 0; s0 < a.b.n_seq; s0 += blockDim.x) {
+      const int s = s0 + threadIdx.x;
+      SeqInfo q{0, 0, 0, 0};
+      if (s < a.b.n_seq) {
+        const SeqView v = seq_view(a.g, a.b, s, report && pass == 0);
+        q.r = v.r;
+        q.c = v.c * a.grp >= a.least ? v.c : 0;  // shorter ones are the decode kernel's
+        q.tok0 = v.tok0;
+      }
+      const int n = q.c == 0 ? 0 : w.tiles(q) * w.nkv * (pass == 0 ? w.span(q) : w.splits(q));
+      int total;
+      q.cum = carry + block_scan(n, sums, &total);
+      if (s < a.b.n_seq) info[s] = q;
+      carry += total;
+      if (pass == 0) {
+        block_scan(q.c == 0 ? 0 : w.tiles(q) * w.nkv, sums, &total);
+        segs += total;
+      }
+    }
+    if (pass == 0) {
+      units = carry;
+      // split along the keys only when whole query tiles would not fill the GPU twice
+      if (segs < 2ll * a.slots) w.kt = max(kMinRun, (int)((units + 2ll * a.slots - 1) / (2ll * a.slots)));
+    }
+    __syncthreads();
+  }
+  w.total = carry;
+  return w;
+}
+
+// ---------------------------------------------------------------- conversion: 64 rows of K and V to operands
+// What a thread (t of 128) holds of a tile before it converts it: K: 32 dims of row t / 2 per group; V: of rows
+// 4 (t % 16) .. + 3 the word t / 16 (8 dims) per group.
+template <int D>
+struct Raw {
+  static constexpr int kGroups = D / 64;
+  uint4 k[kGroups];
+  uint32_t v[kGroups][4];
+  uint32_t kp[kGroups], vp[kGroups][4];
+  int pos;
+  unsigned bad;
+};
+
+template <int D>
+__device__ __forceinline__ void load_raw(Raw<D>& w, const PromptArgs& a, const uint8_t* b0, const uint8_t* b1, int t) {
+  constexpr int kGroups = D / 64;
+  w.bad = (b0 == nullptr ? 1u : 0u) | (b1 == nullptr ? 2u : 0u);
+  const uint8_t* kb = t < 64 ? b0 : b1;         // K row t / 2
+  const uint8_t* vb = (t & 15) < 8 ? b0 : b1;   // V rows 4 (t % 16) ..
+  const int kr = (t >> 1) & 31, vr = 4 * (t & 7), vw = t >> 4;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    w.k[g] = make_uint4(0u, 0u, 0u, 0u);
+    w.kp[g] = 0u;
+    if (kb != nullptr) {
+      w.k[g] = __ldg(reinterpret_cast<const uint4*>(kb + kr * (D / 2) + g * 32 + (t & 1) * 16));
+      w.kp[g] = __ldg(reinterpret_cast<const uint32_t*>(kb + code_bytes(D) + (kr * kGroups + g) * 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w.v[g][i] = w.vp[g][i] = 0u;
+      if (vb != nullptr) {
+        w.v[g][i] = __ldg(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + (vr + i) * (D / 2) + g * 32 + vw * 4));
+        w.vp[g][i] = __ldg(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + code_bytes(D) + ((vr + i) * kGroups + g) * 4));
+      }
+    }
+  }
+  w.pos = 0;
+  if (a.g.track && (t & 1) == 0 && kb != nullptr) w.pos = __ldg(reinterpret_cast<const int*>(kb + pos_at(D) + 4 * kr));
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// The codes i and i + 4 of a word (or, of a permuted word, of two rows), as fp16 less 8 (CENTRE) or as they are.
+template <bool CENTRE>
+__device__ __forceinline__ void code_pairs(uint32_t x, __half2 (&r)[4]) {
+  constexpr float c = CENTRE ? 8.f : 0.f;
+  const __half2 low = __float2half2_rn(-1024.f - c), high = __float2half2_rn(-64.f - c), frac = __float2half2_rn(0.0625f);
+  const uint32_t x8 = x >> 8;
+  r[0] = __hadd2(as_half2((x & 0x000f000fu) | 0x64006400u), low);           // 1024 + code
+  r[1] = __hfma2(as_half2((x & 0x00f000f0u) | 0x64006400u), frac, high);    // 1024 + 16 code
+  r[2] = __hadd2(as_half2((x8 & 0x000f000fu) | 0x64006400u), low);
+  r[3] = __hfma2(as_half2((x8 & 0x00f000f0u) | 0x64006400u), frac, high);
+}
+
+// fp16 (scale, lo) with lo + 15 scale within fp16: a scale that was rounded up may lead beyond, at the type's very end.
+__device__ __forceinline__ uint32_t within(uint32_t pair) {
+  const float2 p = unpack_half(pair);
+  if (fmaf(15.f, p.x, p.y) < 65520.f) return pair;
+  return (pair & 0xffff0000u) | __half_as_ushort(__float2half_rd((65504.f - p.y) / 15.f));
+}
+
+// K of a tile to its stage, and what the softmax has to know: positions, bad pages, V's NaN rows, fp32: the pairs.
+template <int D, bool FP32>
+__device__ __forceinline__ void convert_k(const Raw<D>& w, const PromptArgs& a, unsigned char* kst, unsigned char* smem, int slot, int row0,
+                                          int rows, int t, TileNote* note, int* e_run) {
+  using L = Layout<D, FP32>;
+  constexpr int kGroups = D / 64;
+  const int key = t >> 1, half = t & 1, vk = 4 * (t & 15), vw = t >> 4;
+  const bool kon = row0 + key < rows;
+  if (t < 32) {  // the lanes that own V's rows here (vw 0) are in this warp
+    unsigned long long nan[2] = {0ull, 0ull};
+    if (!FP32 && vw == 0)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row0 + vk + i < rows && (w.vp[g][i] & 0x7fffu) > 0x7c00u) nan[g] |= 1ull << (vk + i);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const unsigned lo = __reduce_or_sync(0xffffffffu, (unsigned)nan[g]), hi = __reduce_or_sync(0xffffffffu, (unsigned)(nan[g] >> 32));
+      if (t == 0) note->nan[g] = (unsigned long long)hi << 32 | lo;
+    }
+    if (t == 0) {
+      if (kGroups == 1) note->nan[1] = 0ull;
+      note->bad = w.bad;
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    // four chunks of 8 dims, in the order 0 4 1 5 2 6 3 7 (q is stored in the same order)
+    unsigned char* kt = kst + g * kKeys * 128 + key * 128;
+    const uint32_t words[4] = {w.k[g].x, w.k[g].y, w.k[g].z, w.k[g].w};
+    const __half2 p = as_half2(kon ? within(w.kp[g]) : 0u), s2 = __low2half2(p), z2 = __high2half2(p);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      __half2 r[4];
+      code_pairs<FP32>(words[c], r);
+      uint4 o;
+      if (FP32) o = make_uint4(as_word(r[0]), as_word(r[1]), as_word(r[2]), as_word(r[3]));
+      else o = make_uint4(as_word(__hfma2(r[0], s2, z2)), as_word(__hfma2(r[1], s2, z2)), as_word(__hfma2(r[2], s2, z2)), as_word(__hfma2(r[3], s2, z2)));
+      *reinterpret_cast<uint4*>(kt + (((4 * half + c) ^ (key & 7)) << 4)) = o;
+    }
+  }
+  if (FP32) {
+    // the rows' pairs, lo moved to the codes' middle, and the largest scale of V
+    float4* pairs = reinterpret_cast<float4*>(smem + L::kPairsAt) + slot * kKeys;
+    if (half == 0) {
+      const float2 p = unpack_half(kon ? w.kp[0] : 0u);
+      *reinterpret_cast<float2*>(&pairs[key].x) = make_float2(p.x, fmaf(8.f, p.x, p.y));
+    }
+    int e = -15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // every warp has all 64 rows: one exponent for all, without a barrier
+      const uint32_t vp = row0 + vk + i < rows ? w.vp[0][i] : 0u;
+      e = max(e, min((int)((vp >> 10) & 31u) - 15, 15));
+      const float2 p = unpack_half(vp);
+      if (vw == 0) *reinterpret_cast<float2*>(&pairs[vk + i].z) = make_float2(p.x, fmaf(8.f, p.x, p.y));
+    }
+    e = (int)__reduce_max_sync(0xffffffffu, (unsigned)(e + 32)) - 32;
+    *e_run = max(*e_run, e);
+    if (t == 0) note->e = *e_run;
+  }
+  if (a.g.track && half == 0) reinterpret_cast<int*>(smem + L::kPosAt)[slot * kKeys + key] = w.pos;
+}
+
+// V of a tile to its stage, transposed: of rows vk .. vk + 3, 8 bytes of each of 8 dims' rows.
+template <int D, bool FP32>
+__device__ __forceinline__ void convert_v(const Raw<D>& w, unsigned char* vst, int row0, int rows, int t) {
+  constexpr int kGroups = D / 64;
+  const int vk = 4 * (t & 15), vw = t >> 4;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    unsigned char* vt = vst + (g * 64 + vw * 8) * 128;
+    __half2 s01{}, s23{}, z01{}, z23{};
+    if (!FP32) {
+      uint32_t vp[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // rows behind the end, and NaN groups (which the softmax is told of), are zeros
+        vp[i] = row0 + vk + i < rows && (w.vp[g][i] & 0x7fffu) <= 0x7c00u ? within(w.vp[g][i]) : 0u;
+      s01 = as_half2(__byte_perm(vp[0], vp[1], 0x5410));
+      z01 = as_half2(__byte_perm(vp[0], vp[1], 0x7632));
+      s23 = as_half2(__byte_perm(vp[2], vp[3], 0x5410));
+      z23 = as_half2(__byte_perm(vp[2], vp[3], 0x7632));
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint32_t sel = hf ? 0x7632u : 0x5410u;
+      __half2 x[4], y[4];
+      code_pairs<FP32>(__byte_perm(w.v[g][0], w.v[g][1], sel), x);
+      code_pairs<FP32>(__byte_perm(w.v[g][2], w.v[g][3], sel), y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int dim = 4 * hf + j;  // row of the tile: g * 64 + 8 vw + dim; its low three bits are dim
+        uint2 o;
+        if (FP32) o = make_uint2(as_word(x[j]), as_word(y[j]));
+        else o = make_uint2(as_word(__hfma2(x[j], s01, z01)), as_word(__hfma2(y[j], s23, z23)));
+        *reinterpret_cast<uint2*>(vt + dim * 128 + (((vk >> 3) ^ dim) << 4) + (vk & 4) * 2) = o;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D, bool FP32, bool FEAT>
+__global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_constant__ PromptArgs a) {
+  using L = Layout<D, FP32>;
+  constexpr int kGroups = D / 64;
+  extern __shared__ unsigned char raw_smem[];
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, pv_done, q_full, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ unsigned failed;
+  __shared__ TileNote notes[kNotes];
+  __shared__ int sums[kThreads / 32];
+  unsigned char* smem = raw_smem + ((1024u - (smem_of(raw_smem) & 1023u)) & 1023u);
+  SeqInfo* info = reinterpret_cast<SeqInfo*>(smem + L::kInfoAt);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 128);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 128);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 2);
+    }
+    mbar_init(&drain, 1);
+    mbar_init(&p_full, 128);
+    mbar_init(&pv_done, 1);
+    mbar_init(&q_full, 128);
+    failed = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 7) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&tmem_slot)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const Work work = make_work(a, info, sums, blockIdx.x == 0);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+  const uint32_t t_out = tmem + 2 * kKeys, t_sum = t_out + 64;  // fp32: sums behind the output
+  volatile unsigned* abort = &failed;
+  unsigned tile_no = 0;  // key tiles so far: every role counts them alike
+
+  if (warp >= 4) {
+    // ------------------------------------------------------------ conversion and matrix instructions
+    const int t = threadIdx.x - 128;
+    bool ok = true;
+    const uint32_t sq_at = smem_of(smem + L::kQAt), sp_at = smem_of(smem + L::kPAt), k_at = smem_of(smem + L::kKAt), v_at = smem_of(smem + L::kVAt);
+    unsigned items = 0;
+    // (lane 0 of warp 4) S = Q K^T of key tile number `no`, the item's j-th
+    auto score = [&](unsigned no, int j) {
+      if (j == 0 && !mbar_wait(&q_full, items & 1, abort)) return false;
+      if (!mbar_wait(&k_full[no & 1], (no >> 1) & 1, abort)) return false;
+      fence_after();
+      const uint32_t kt = k_at + (no & 1) * L::kTile, d = tmem + (no & 1) * kKeys;
+#pragma unroll
+      for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma(d, tile_desc(sq_at + (hf * kGroups + g) * kQ * 128 + ks * 32), tile_desc(kt + g * kKeys * 128 + ks * 32), idesc(kKeys),
+                 hf + g + ks > 0 ? 1u : 0u);
+      umma_commit(&k_empty[no & 1]);
+      umma_commit(&s_full[no & 1]);
+      mbar_arrive(&s_full[no & 1]);  // and orders the conversion's notes before the softmax
+      return true;
+    };
+    // (the same lane) O += P V
+    auto product = [&](unsigned no, int j) {
+      const int vs = L::kVStages == 2 ? no & 1 : 0;
+      if (!mbar_wait(&v_full[vs], (no / L::kVStages) & 1, abort) || !mbar_wait(&p_full, no & 1, abort)) return false;
+      fence_after();
+      const uint32_t vt = v_at + vs * L::kTile;
+      const bool fresh = FP32 ? j % kFlush == 0 : j == 0;
+#pragma unroll
+      for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma(t_out, tile_desc(sp_at + hf * kQ * 128 + ks * 32), tile_desc(vt + ks * 32), idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
+      umma_commit(&v_empty[vs]);
+      umma_commit(&pv_done);
+      return true;
+    };
+    for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+      const Item it = item_at(work, i);
+      if (it.k0 >= it.k1) continue;
+      const SeqInfo sq = info[it.s];
+      const int32_t* table = a.b.tables + (size_t)it.s * a.g.max_pages;
+      // the page numbers are asked for one tile before the rows, the rows one tile before they are converted
+      auto page = [&](int row) { return row < sq.r ? table[row >> a.g.page_shift] : -1; };
+      auto block = [&](int row, int pg) -> const uint8_t* {
+        if (row >= sq.r) return nullptr;
+        if ((unsigned)pg >= (unsigned)a.g.num_pages) {
+          if (t == 0) flag(a.b.status, MBK_KV4_BAD_PAGE);
+          return nullptr;
+        }
+        return a.g.pool + (size_t)pg * a.g.page_stride + (size_t)(a.layer * a.g.nkv + it.h) * a.g.head_stride +
+               (unsigned)(((row & ((1 << a.g.page_shift) - 1)) / kRows) * a.g.block_bytes);
+      };
+      Raw<D> cur;
+      {
+        const int r = it.k0 * kKeys;
+        load_raw<D>(cur, a, block(r, page(r)), block(r + kRows, page(r + kRows)), t);
+      }
+      int p0 = page((it.k0 + 1) * kKeys), p1 = page((it.k0 + 1) * kKeys + kRows);
+      int e_run = -15;
+      for (int k = it.k0; k < it.k1; ++k, ++tile_no) {
+        Raw<D> nxt;
+        if (k + 1 < it.k1) {
+          const int r = (k + 1) * kKeys;
+          load_raw<D>(nxt, a, block(r, p0), block(r + kRows, p1), t);
+          p0 = page(r + kKeys);
+          p1 = page(r + kKeys + kRows);
+        }
+        const int st = tile_no & 1, vs = L::kVStages == 2 ? st : 0, slot = tile_no % kNotes;
+        const unsigned vn = tile_no / L::kVStages;  // how often V's stage was used before
+        cur.bad &= k * kKeys + kRows < sq.r ? 3u : 1u;  // a block behind the cache's end has no page: not an error
+        if (tile_no >= 2 && !(ok = warp_wait(&k_empty[st], ((tile_no >> 1) - 1) & 1, abort))) break;
+        convert_k<D, FP32>(cur, a, smem + L::kKAt + st * L::kTile, smem, slot, k * kKeys, sq.r, t, &notes[slot], &e_run);
+        fence_async();
+        mbar_arrive(&k_full[st]);
+        auto value = [&] {
+          if (vn >= 1 && !warp_wait(&v_empty[vs], (vn - 1) & 1, abort)) return false;
+          convert_v<D, FP32>(cur, smem + L::kVAt + vs * L::kTile, k * kKeys, sq.r, t);
+          fence_async();
+          mbar_arrive(&v_full[vs]);
+          return true;
+        };
+        // with one stage of V the product before has to be under way before V's turn comes
+        if (L::kVStages == 2 && !(ok = value())) break;
+        if (t == 0) ok = score(tile_no, k - it.k0) && (k == it.k0 || product(tile_no - 1, k - it.k0 - 1));
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (L::kVStages == 1 && !(ok = value())) break;
+        cur = nxt;
+      }
+      if (ok && t == 0) ok = product(tile_no - 1, it.k1 - it.k0 - 1);
+      ok = __all_sync(0xffffffffu, ok);
+      ++items;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: one query row a thread
+    const int row = threadIdx.x;
+    const uint32_t lane_at = (uint32_t)(warp * 32) << 16;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+      const Item it = item_at(work, i);
+      const SeqInfo sq = info[it.s];
+      if (it.k0 >= it.k1 && (it.parts > 0 || it.split > 0)) continue;
+      const int qrow = it.tile * kQ + row, tok = qrow / a.grp, head = it.h * a.grp + qrow - tok * a.grp;
+      const bool on = tok < sq.c;
+      const int limit = on ? sq.r - sq.c + tok : -1;
+      const int first_limit = sq.r - sq.c + it.tile * kQ / a.grp;
+      const bool whole_tile = (it.tile + 1) * kQ <= sq.c * a.grp;
+      const int qpos = FEAT && on ? (a.b.positions != nullptr ? a.b.positions[it.s] : sq.r - sq.c) + tok : 0;
+      const float slope = FEAT && on && a.a.slopes != nullptr ? a.a.slopes[head] * kLog2e : 0.f;
+      // the row of q to the operand, its largest element scaled to [2^13, 2^14)
+      float mul, addm = 0.f;  // score = mul * (acc, or fp32: scale_r acc + z_r addm)
+      {
+        float mx = 0.f, sum = 0.f;
+        const size_t at = (size_t)(sq.tok0 + (on ? tok : 0)) * a.a.ldq + (size_t)head * D;
+        auto load = [&](int c, float(&x)[8]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.f;
+          if (on) {
+            if (FP32) load8<float>(reinterpret_cast<const float*>(a.a.q) + at + 8 * c, x);
+            else load8<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.a.q) + at + 8 * c, x);
+          }
+        };
+        for (int c = 0; c < D / 8; ++c) {
+          float x[8];
+          load(c, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            mx = fmaxf(mx, fabsf(x[e]));
+            sum += x[e];
+          }
+        }
+        int ex = (__float_as_int(mx) >> 23) & 255;
+        ex = ex == 255 ? 140 : max(ex, 20);
+        const float up = a.scale2 < 0.f ? -pow2i(140 - ex) : pow2i(140 - ex);  // mul >= 0: the largest acc is the largest score
+        mul = pow2i(ex - 140) * fabsf(a.scale2);
+        if (FP32) addm = sum * up;
+        for (int c = 0; c < D / 8; ++c) {
+          float x[8];
+          load(c, x);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // the conversion's order of dims: 0 4 1 5 2 6 3 7
+            const float x0 = x[e] * up, x1 = x[e + 4] * up;
+            hi[e] = pack_half(x0, x1);
+            const float2 u = unpack_half(hi[e]);
+            lo[e] = pack_half(x0 - u.x, x1 - u.y);
+          }
+          unsigned char* q = smem + L::kQAt + (c >> 3) * kQ * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (FP32) *reinterpret_cast<uint4*>(q + kGroups * kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      if (it.k0 < it.k1) {
+        fence_async();
+        mbar_arrive(&q_full);
+      }
+      float m = -INFINITY, l = 0.f, z = 0.f;
+      int e_cur = -15;
+      unsigned nan_groups = 0u;
+      for (int k = it.k0; k < it.k1; ++k, ++tile_no) {
+        const int st = tile_no & 1, slot = tile_no % kNotes, j = k - it.k0;
+        if (!(ok = warp_wait(&s_full[st], (tile_no >> 1) & 1, abort))) break;
+        fence_after();
+        float x[kKeys];
+        tmem_ld32(tmem + lane_at + st * kKeys, x);
+        tmem_ld32(tmem + lane_at + st * kKeys + 32, x + 32);
+        tmem_wait_ld();
+        const float4* pairs = reinterpret_cast<const float4*>(smem + L::kPairsAt) + slot * kKeys;
+        const unsigned bad = notes[slot].bad;
+        if (FP32)
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) {
+            const float2 p = *reinterpret_cast<const float2*>(&pairs[c].x);
+            x[c] = fmaf(p.x, x[c], p.y * addm);
+          }
+        float mulx = mul;
+        if (FEAT) {
+          mulx = 1.f;
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) x[c] *= mul;
+          if (a.a.cap > 0.f) {
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c) {
+              const float e = ex2(fminf(x[c] * a.cap_in, 126.f));
+              x[c] = fmaf(-a.cap_out, __fdividef(2.f, 1.f + e), a.cap_out);
+            }
+          }
+          if (a.a.slopes != nullptr || a.a.window > 0) {
+            const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys;
+            const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c) {
+              const int gap = (a.g.track ? pos[c] : k * kKeys + c) - qpos;
+              x[c] = fmaf(slope, (float)gap, x[c]);
+              x[c] = gap <= win ? -INFINITY : x[c];
+            }
+          }
+        }
+        if ((k + 1) * kKeys - 1 > first_limit || !whole_tile || bad != 0u) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (k * kKeys + c > limit || ((bad >> (c >> 5)) & 1u)) x[c] = -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int c = 1; c < kKeys; ++c) top = fmaxf(top, x[c]);
+        top = top == -INFINITY ? top : top * mulx;
+        float rescale = 1.f;
+        bool renew = top > m + kSlack;
+        int e_new = e_cur;
+        if (FP32) {
+          e_new = notes[slot].e;
+          renew = renew || e_new != e_cur;
+        }
+        const bool any = __any_sync(0xffffffffu, renew);
+        if (any) {
+          const float nm = fmaxf(m, top);
+          rescale = nm == -INFINITY ? 1.f : ex2(m - nm);
+          m = nm;
+          l *= rescale;
+          z *= rescale;
+          if (FP32) rescale *= pow2i(e_cur - e_new);
+          e_cur = e_new;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const float unit = FP32 ? pow2i(6 - e_cur) : 1.f;  // fp32: weights are held as p scale_r 2^(6 - e): below 2^15
+        if (!FP32 && (notes[slot].nan[0] | notes[slot].nan[kGroups - 1]) != 0ull) {
+          // rows of V that are NaN: the output of those who see them is NaN
+          const unsigned long long n0 = notes[slot].nan[0], n1 = notes[slot].nan[kGroups - 1];
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (x[c] > -INFINITY || x[c] != x[c]) nan_groups |= (unsigned)(n0 >> c & 1ull) | (unsigned)(n1 >> c & 1ull) << 1;
+        }
+        // the product before has read the weights and left the output
+        if (j > 0 && !(ok = warp_wait(&pv_done, (tile_no - 1) & 1, abort))) break;
+        fence_after();
+        if (j > 0) {
+          if (FP32 && j % kFlush == 0) {  // move the output to the sums
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
+              float o[16], s[16];
+              tmem_ld16(t_out + lane_at + c, o);
+              if (j > kFlush) tmem_ld16(t_sum + lane_at + c, s);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = (j > kFlush ? o[e] + s[e] : o[e]) * rescale;
+              tmem_st16(t_sum + lane_at + c, o);
+            }
+            tmem_wait_st();
+          } else if (any) {
+#pragma unroll 1
+            for (int c = 0; c < (FP32 && j > kFlush ? 128 : D); c += 16) {
+              float o[16];
+              tmem_ld16(t_out + lane_at + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= rescale;
+              tmem_st16(t_out + lane_at + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        unsigned char* p = smem + L::kPAt + row * 128;
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i0 = c + 2 * e, i1 = i0 + 1;
+            float p0 = ex2(fmaf(x[i0], mulx, -base)), p1 = ex2(fmaf(x[i1], mulx, -base));
+            l += p0;
+            l += p1;
+            if (FP32) {
+              const float2 v0 = *reinterpret_cast<const float2*>(&pairs[i0].z), v1 = *reinterpret_cast<const float2*>(&pairs[i1].z);
+              // a weight of zero (a masked row) takes nothing of its row, NaN included
+              z += p0 > 0.f ? p0 * v0.y : p0;
+              z += p1 > 0.f ? p1 * v1.y : p1;
+              p0 = p0 > 0.f ? p0 * (v0.x * unit) : p0;
+              p1 = p1 > 0.f ? p1 * (v1.x * unit) : p1;
+            }
+            hi[e] = pack_half(p0, p1);
+            if (FP32) {
+              const float2 u = unpack_half(hi[e]);
+              lo[e] = pack_half(p0 - u.x, p1 - u.y);
+            }
+          }
+          unsigned char* at = p + (((c >> 3) ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (FP32) *reinterpret_cast<uint4*>(at + kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async();
+        fence_before();
+        mbar_arrive(&p_full);
+      }
+      if (!ok) break;
+      const int n = it.k1 - it.k0;
+      if (n > 0) {
+        if (!(ok = warp_wait(&pv_done, (tile_no - 1) & 1, abort))) break;
+        fence_after();
+      }
+      // the output, or the run's partial
+      const bool last = it.parts <= 1;
+      const float inv = last ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const float unit = FP32 ? pow2i(e_cur - 6) : 1.f;
+      float* part = last ? nullptr : a.part + ((size_t)i * kQ + row) * (D + 4);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float o[16], s[16];
+        __syncwarp();
+        if (n > 0) {
+          tmem_ld16(t_out + lane_at + c, o);
+          if (FP32 && n > kFlush) tmem_ld16(t_sum + lane_at + c, s);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (FP32 && n > kFlush) o[e] += s[e];
+          o[e] = n > 0 ? (FP32 ? fmaf(o[e], unit, z) : o[e]) * inv : 0.f;
+          if (!FP32 && (nan_groups >> (c >> 6) & 1u)) o[e] = NAN;
+        }
+        if (on) {
+          float y0[8], y1[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y0[e] = o[e];
+            y1[e] = o[8 + e];
+          }
+          if (last) {
+            const size_t at = (size_t)(sq.tok0 + tok) * a.a.ldo + (size_t)head * D + c;
+            store_out(a.a, at, y0);
+            store_out(a.a, at + 8, y1);
+          } else {
+            store8(part + c, y0);
+            store8(part + c + 8, y1);
+          }
+        }
+      }
+      if (on) {
+        if (!last) {
+          part[D] = m;
+          part[D + 1] = l;
+        } else if (a.lse != nullptr) {
+          a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = l > 0.f ? m + log2f(l) : INFINITY;
+        }
+      }
+      __syncwarp();
+      fence_before();  // the output has been read before the next item's first product
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (failed != 0u && threadIdx.x == 0) flag(a.b.status, MBK_KV4_TIMEOUT);
+  if (failed != 0u && warp == 4 && lane == 0) {
+    // matrix instructions in flight end before their tensor memory is freed
+    umma_commit(&drain);
+    for (int i = 0; i < 20000000 && !mbar_test(&drain, 0); ++i) {
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 7) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the runs of query tiles whose keys were split.
+template <int D>
+__global__ void __launch_bounds__(512) prompt_combine_kernel(const __grid_constant__ PromptArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int sums[16];
+  const Work w = make_work(a, reinterpret_cast<SeqInfo*>(smem), sums, false);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = blockIdx.x; i < w.total; i += gridDim.x) {
+    const Item it = item_at(w, i);
+    if (it.split != 0 || it.parts <= 1) continue;
+    const SeqInfo sq = w.seq[it.s];
+    // the splits of a (tile, head) are nkv items apart
+    join<D>(a, sq, it.h, it.tile * kQ, min(kQ, sq.c * a.grp - it.tile * kQ), it.parts, nullptr,
+            [&](int k) { return a.part + (size_t)(i + k * w.nkv) * kQ * (D + 4); });
+  }
+}
+
+template <int D, bool FP32, bool FEAT>
+cudaError_t run(const PromptArgs& a, cudaStream_t st) {
+  static std::atomic<bool> once[64];
+  const size_t smem = 1024 + Layout<D, FP32>::kInfoAt + (size_t)a.b.n_seq * sizeof(SeqInfo);
+  if (cudaError_t e = allow_smem((const void*)prompt_kernel<D, FP32, FEAT>, once, 112 * 1024)) return e;
+  const long long tiles = ((long long)a.b.max_count * a.grp + kQ - 1) / kQ;
+  const long long items = a.b.n_seq * (long long)a.g.nkv * tiles * ((a.b.max_rows + kKeys - 1) / kKeys / kMinRun + 1);
+  const int grid = (int)std::max<long long>(1, std::min<long long>(a.slots, items));
+  if (cudaError_t e = launch(prompt_kernel<D, FP32, FEAT>, dim3(grid), kThreads, smem, st, false, a)) return e;
+  return launch(prompt_combine_kernel<D>, dim3((unsigned)a.slots), 512, (size_t)a.b.n_seq * sizeof(SeqInfo), st, true, a);
+}
+
+}  // namespace
+
+size_t kv4_prompt_partials(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
+  // whole query tiles below 2 x slots, their runs below 4 x slots (and none split otherwise)
+  const long long tiles = ((long long)b.max_count * (g.nq / g.nkv) + kQ - 1) / kQ * g.nkv * b.n_seq;
+  const long long runs = (b.max_rows + kKeys - 1) / kKeys / kMinRun + 1;
+  return (size_t)std::min<long long>(4ll * 2 * num_sms, tiles * runs) * kQ * (g.d + 4) * 4;
+}
+
+cudaError_t kv4_prompt(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4Attn& at, int least, float* part, float* lse, int num_sms,
+                       cudaStream_t st) {
+  PromptArgs a;
+  a.g = g;
+  a.b = b;
+  a.a = at;
+  a.layer = layer;
+  a.grp = g.nq / g.nkv;
+  a.least = least;
+  a.slots = 2 * num_sms;
+  a.scale2 = at.scale * kLog2e;
+  a.cap_in = at.cap > 0.f ? 2.f / at.cap : 0.f;
+  a.cap_out = at.cap * kLog2e;
+  a.part = part;
+  a.lse = lse;
+  // (a scale of zero times a masked score of -inf would be NaN: the general path scales first)
+  const bool feat = at.cap > 0.f || at.slopes != nullptr || at.window > 0 || at.scale == 0.f;
+  if (!at.bf16) return feat ? run<64, true, true>(a, st) : run<64, true, false>(a, st);
+  if (g.d == 64) return feat ? run<64, false, true>(a, st) : run<64, false, false>(a, st);
+  return feat ? run<128, false, true>(a, st) : run<128, false, false>(a, st);
+}
+
+}  // namespace mbk
