@@ -13,7 +13,7 @@
 //   fp32 (head dim 64): the operands are code - 8, exact; q and the weights are hi + lo fp16 (22 bits); the
 // softmax applies the rows' scale and lo, as the decode kernel does.  The tensor cores' sums are truncated, so the
 // output is moved to a second buffer and added there in fp32 every 8 tiles.
-//   Bound by the softmax: 64 exponentials and about 6 (fp32: 13) instructions each per row and tile.
+//   Bound by the softmax's instructions, which therefore go two values at a time where the GPU has a form for it.
 #include "mbk_kv4_device.h"
 #include "mbk_kv4_split.h"
 
@@ -25,6 +25,7 @@ constexpr int kKeys = 64;      // cache rows of a key tile: one 128-byte row of 
 constexpr int kThreads = 256;  // softmax 128, conversion 128
 constexpr int kTmemCols = 256; // scores 2 x 64, output 64 or 128, fp32: sums 64
 constexpr int kFlush = 8;      // fp32: tiles between two moves of the output
+constexpr int kMaxRounds = 4;  // items per CTA at most, about, where keys are split
 constexpr int kNotes = 4;      // tiles whose notes and pairs are kept
 constexpr float kSlack = 8.f;  // a running maximum is renewed when a score exceeds it by 2^8
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -89,8 +90,41 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Two fp32 values in a register pair, and the instructions on both at once.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair_of(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 sum2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // 32 columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float* v) {
+__device__ __forceinline__ void tmem_ld32(uint32_t at, f2* v) {
   uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -101,7 +135,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float* v) {
         "=r"(r[31])
       : "r"(at));
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld16(uint32_t at, float (&v)[16]) {
@@ -134,7 +168,7 @@ struct Layout {
   static constexpr int kTile = kKeys * 128 * kGroups;           // K: per group [64 rows][64 dims]; V: [D dims][64 rows]
   static constexpr int kVStages = D == 64 ? 2 : 1;
   static constexpr int kQAt = 0, kPAt = kQBytes, kKAt = kPAt + kPBytes, kVAt = kKAt + 2 * kTile;
-  static constexpr int kPairsAt = kVAt + kVStages * kTile;      // fp32: float4 (sk, zk, sv, zv) [kNotes][64]
+  static constexpr int kPairsAt = kVAt + kVStages * kTile;      // fp32: float [kNotes][4: sk, zk, sv, zv][64]
   static constexpr int kPosAt = kPairsAt + (FP32 ? kNotes * kKeys * 16 : 0);
   static constexpr int kInfoAt = kPosAt + kNotes * kKeys * 4;   // then SeqInfo [n_seq]
 };
@@ -144,7 +178,7 @@ struct Layout {
 struct TileNote {
   unsigned bad;                // bit b: block b of the tile lies in a page outside the pool
   int e;                       // fp32: exponent of the largest scale of V so far
-  unsigned long long nan[2];   // bf16: rows whose V is NaN, per group of 64 dims (the operand has zeros there)
+  unsigned long long nan[2];   // rows whose V is NaN, per group of 64 dims (they are zero for the products)
 };
 
 // ---------------------------------------------------------------- work items
@@ -230,8 +264,30 @@ __device__ Work make_work(const PromptArgs& a, SeqInfo* info, int* sums, bool re
     }
     if (pass == 0) {
       units = carry;
-      // split along the keys only when whole query tiles would not fill the GPU twice
-      if (segs < 2ll * a.slots) w.kt = max(kMinRun, (int)((units + 2ll * a.slots - 1) / (2ll * a.slots)));
+      // Split along the keys only when whole query tiles would not fill the GPU twice, into runs of the length
+      // that ends first: rounds of items on all slots, each run costing its tiles and about 3 more.
+      if (segs < 2ll * a.slots) {
+        long long best = -1;
+        int run = 0;
+        for (int rounds = 1; rounds <= kMaxRounds; ++rounds) {
+          w.kt = max(kMinRun, (int)((units + (long long)rounds * a.slots - 1) / ((long long)rounds * a.slots)));
+          int items = 0;
+          for (int s0 = 0; s0 < a.b.n_seq; s0 += blockDim.x) {
+            const int s = s0 + threadIdx.x;
+            const SeqInfo q = s < a.b.n_seq ? info[s] : SeqInfo{0, 0, 0, 0};
+            int total;
+            block_scan(q.c == 0 ? 0 : w.tiles(q) * w.nkv * w.splits(q), sums, &total);
+            items += total;
+          }
+          const long long cost = (long long)((items + a.slots - 1) / a.slots) * (w.kt + 3);
+          if (best < 0 || cost < best) {
+            best = cost;
+            run = w.kt;
+          }
+          if (w.kt == kMinRun) break;
+        }
+        w.kt = run;
+      }
     }
     __syncthreads();
   }
@@ -297,8 +353,9 @@ __device__ __forceinline__ void code_pairs(uint32_t x, __half2 (&r)[4]) {
 
 // fp16 (scale, lo) with lo + 15 scale within fp16: a scale that was rounded up may lead beyond, at the type's very end.
 __device__ __forceinline__ uint32_t within(uint32_t pair) {
+  if ((pair & 0x7fffu) < 0x6800u && (pair >> 16 & 0x7fffu) < 0x7800u) return pair;  // below 2^11 and 2^15: far from it
   const float2 p = unpack_half(pair);
-  if (fmaf(15.f, p.x, p.y) < 65520.f) return pair;
+  if (!(fmaf(15.f, p.x, p.y) >= 65520.f)) return pair;
   return (pair & 0xffff0000u) | __half_as_ushort(__float2half_rd((65504.f - p.y) / 15.f));
 }
 
@@ -312,7 +369,7 @@ __device__ __forceinline__ void convert_k(const Raw<D>& w, const PromptArgs& a, 
   const bool kon = row0 + key < rows;
   if (t < 32) {  // the lanes that own V's rows here (vw 0) are in this warp
     unsigned long long nan[2] = {0ull, 0ull};
-    if (!FP32 && vw == 0)
+    if (vw == 0)
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
 #pragma unroll
@@ -345,22 +402,32 @@ __device__ __forceinline__ void convert_k(const Raw<D>& w, const PromptArgs& a, 
     }
   }
   if (FP32) {
-    // the rows' pairs, lo moved to the codes' middle, and the largest scale of V
-    float4* pairs = reinterpret_cast<float4*>(smem + L::kPairsAt) + slot * kKeys;
+    // the rows' pairs, lo moved to the codes' middle; V's scales in units of 2^(e - 6), e being the exponent of the
+    // largest so far, so that scale times a weight of at most 2^8 stays below 2^15
+    float* pairs = reinterpret_cast<float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
     if (half == 0) {
       const float2 p = unpack_half(kon ? w.kp[0] : 0u);
-      *reinterpret_cast<float2*>(&pairs[key].x) = make_float2(p.x, fmaf(8.f, p.x, p.y));
+      pairs[key] = p.x;
+      pairs[kKeys + key] = fmaf(8.f, p.x, p.y);
     }
     int e = -15;
+    uint32_t vp[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // every warp has all 64 rows: one exponent for all, without a barrier
-      const uint32_t vp = row0 + vk + i < rows ? w.vp[0][i] : 0u;
-      e = max(e, min((int)((vp >> 10) & 31u) - 15, 15));
-      const float2 p = unpack_half(vp);
-      if (vw == 0) *reinterpret_cast<float2*>(&pairs[vk + i].z) = make_float2(p.x, fmaf(8.f, p.x, p.y));
+      vp[i] = row0 + vk + i < rows && (w.vp[0][i] & 0x7fffu) <= 0x7c00u ? w.vp[0][i] : 0u;
+      e = max(e, min((int)((vp[i] >> 10) & 31u) - 15, 15));
     }
     e = (int)__reduce_max_sync(0xffffffffu, (unsigned)(e + 32)) - 32;
     *e_run = max(*e_run, e);
+    if (vw == 0) {
+      const float unit = pow2i(6 - *e_run);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack_half(vp[i]);
+        pairs[2 * kKeys + vk + i] = p.x * unit;
+        pairs[3 * kKeys + vk + i] = fmaf(8.f, p.x, p.y);
+      }
+    }
     if (t == 0) note->e = *e_run;
   }
   if (a.g.track && half == 0) reinterpret_cast<int*>(smem + L::kPosAt)[slot * kKeys + key] = w.pos;
@@ -557,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       const bool on = tok < sq.c;
       const int limit = on ? sq.r - sq.c + tok : -1;
       const int first_limit = sq.r - sq.c + it.tile * kQ / a.grp;
+      const int last_limit = sq.r - sq.c + min(sq.c - 1, (it.tile * kQ + kQ - 1) / a.grp);
       const bool whole_tile = (it.tile + 1) * kQ <= sq.c * a.grp;
       const int qpos = FEAT && on ? (a.b.positions != nullptr ? a.b.positions[it.s] : sq.r - sq.c) + tok : 0;
       const float slope = FEAT && on && a.a.slopes != nullptr ? a.a.slopes[head] * kLog2e : 0.f;
@@ -607,56 +675,78 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
         fence_async();
         mbar_arrive(&q_full);
       }
-      float m = -INFINITY, l = 0.f, z = 0.f;
+      float m = -INFINITY;
+      f2 l = 0ull, z = 0ull;  // two partial sums each
       int e_cur = -15;
       unsigned nan_groups = 0u;
       for (int k = it.k0; k < it.k1; ++k, ++tile_no) {
         const int st = tile_no & 1, slot = tile_no % kNotes, j = k - it.k0;
         if (!(ok = warp_wait(&s_full[st], (tile_no >> 1) & 1, abort))) break;
         fence_after();
-        float x[kKeys];
+        f2 x[kKeys / 2];
         tmem_ld32(tmem + lane_at + st * kKeys, x);
-        tmem_ld32(tmem + lane_at + st * kKeys + 32, x + 32);
+        tmem_ld32(tmem + lane_at + st * kKeys + 32, x + 16);
         tmem_wait_ld();
-        const float4* pairs = reinterpret_cast<const float4*>(smem + L::kPairsAt) + slot * kKeys;
+        const float* pairs = reinterpret_cast<const float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
         const unsigned bad = notes[slot].bad;
-        if (FP32)
+        if (FP32) {
+          const f2 add = pair_of(addm, addm);
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) {
-            const float2 p = *reinterpret_cast<const float2*>(&pairs[c].x);
-            x[c] = fmaf(p.x, x[c], p.y * addm);
+          for (int c = 0; c < kKeys / 2; c += 2) {
+            const ulonglong2 sk = *reinterpret_cast<const ulonglong2*>(pairs + 2 * c), zk = *reinterpret_cast<const ulonglong2*>(pairs + kKeys + 2 * c);
+            x[c] = fma2(sk.x, x[c], mul2(zk.x, add));
+            x[c + 1] = fma2(sk.y, x[c + 1], mul2(zk.y, add));
           }
+        }
         float mulx = mul;
         if (FEAT) {
           mulx = 1.f;
+          if (a.a.cap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap))
+            const f2 in = pair_of(mul * a.cap_in, mul * a.cap_in), one = pair_of(1.f, 1.f), out = pair_of(a.cap_out, a.cap_out),
+                     out2 = pair_of(-2.f * a.cap_out, -2.f * a.cap_out);
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) x[c] *= mul;
-          if (a.a.cap > 0.f) {
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c) {
-              const float e = ex2(fminf(x[c] * a.cap_in, 126.f));
-              x[c] = fmaf(-a.cap_out, __fdividef(2.f, 1.f + e), a.cap_out);
+            for (int c = 0; c < kKeys / 2; ++c) {
+              float2 e = halves(mul2(x[c], in));
+              e = halves(sum2(pair_of(ex2(e.x), ex2(e.y)), one));
+              x[c] = fma2(pair_of(rcp(e.x), rcp(e.y)), out2, out);
             }
+          } else {
+            const f2 by = pair_of(mul, mul);
+#pragma unroll
+            for (int c = 0; c < kKeys / 2; ++c) x[c] = mul2(x[c], by);
           }
-          if (a.a.slopes != nullptr || a.a.window > 0) {
+          // distances, where there is a bias, or a window that leaves out some row of the tile for some query
+          if (a.a.slopes != nullptr || (a.a.window > 0 && (a.g.track || k * kKeys <= last_limit - a.a.window))) {
             const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys;
             const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c) {
-              const int gap = (a.g.track ? pos[c] : k * kKeys + c) - qpos;
-              x[c] = fmaf(slope, (float)gap, x[c]);
-              x[c] = gap <= win ? -INFINITY : x[c];
+            for (int c = 0; c < kKeys / 2; ++c) {
+              float2 v = halves(x[c]);
+              const int g0 = (a.g.track ? pos[2 * c] : k * kKeys + 2 * c) - qpos, g1 = (a.g.track ? pos[2 * c + 1] : k * kKeys + 2 * c + 1) - qpos;
+              v.x = g0 <= win ? -INFINITY : fmaf(slope, (float)g0, v.x);
+              v.y = g1 <= win ? -INFINITY : fmaf(slope, (float)g1, v.y);
+              x[c] = pair_of(v.x, v.y);
             }
           }
         }
         if ((k + 1) * kKeys - 1 > first_limit || !whole_tile || bad != 0u) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (k * kKeys + c > limit || ((bad >> (c >> 5)) & 1u)) x[c] = -INFINITY;
+          for (int c = 0; c < kKeys / 2; ++c) {
+            float2 v = halves(x[c]);
+            const bool off = (bad >> (c >> 4)) & 1u;
+            if (off || k * kKeys + 2 * c > limit) v.x = -INFINITY;
+            if (off || k * kKeys + 2 * c + 1 > limit) v.y = -INFINITY;
+            x[c] = pair_of(v.x, v.y);
+          }
         }
-        float top = x[0];
+        float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-        for (int c = 1; c < kKeys; ++c) top = fmaxf(top, x[c]);
+        for (int c = 0; c < kKeys / 2; c += 2) {
+          const float2 v = halves(x[c]), u = halves(x[c + 1]);
+          top = fmaxf(top, fmaxf(v.x, v.y));
+          top1 = fmaxf(top1, fmaxf(u.x, u.y));
+        }
+        top = fmaxf(top, top1);
         top = top == -INFINITY ? top : top * mulx;
         float rescale = 1.f;
         bool renew = top > m + kSlack;
@@ -670,19 +760,22 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
           const float nm = fmaxf(m, top);
           rescale = nm == -INFINITY ? 1.f : ex2(m - nm);
           m = nm;
-          l *= rescale;
-          z *= rescale;
+          l = mul2(l, pair_of(rescale, rescale));
+          z = mul2(z, pair_of(rescale, rescale));
           if (FP32) rescale *= pow2i(e_cur - e_new);
           e_cur = e_new;
         }
         const float base = m == -INFINITY ? 0.f : m;
-        const float unit = FP32 ? pow2i(6 - e_cur) : 1.f;  // fp32: weights are held as p scale_r 2^(6 - e): below 2^15
-        if (!FP32 && (notes[slot].nan[0] | notes[slot].nan[kGroups - 1]) != 0ull) {
+        if ((notes[slot].nan[0] | notes[slot].nan[1]) != 0ull) {
           // rows of V that are NaN: the output of those who see them is NaN
-          const unsigned long long n0 = notes[slot].nan[0], n1 = notes[slot].nan[kGroups - 1];
+          const unsigned long long n0 = notes[slot].nan[0], n1 = notes[slot].nan[1];
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (x[c] > -INFINITY || x[c] != x[c]) nan_groups |= (unsigned)(n0 >> c & 1ull) | (unsigned)(n1 >> c & 1ull) << 1;
+          for (int c = 0; c < kKeys / 2; ++c) {
+            const float2 v = halves(x[c]);
+            const unsigned b0 = (unsigned)(n0 >> (2 * c)) & 3u, b1 = (unsigned)(n1 >> (2 * c)) & 3u;
+            if (!(v.x == -INFINITY)) nan_groups |= (b0 & 1u) | (b1 & 1u) << 1;
+            if (!(v.y == -INFINITY)) nan_groups |= (b0 >> 1) | (b1 & 2u);
+          }
         }
         // the product before has read the weights and left the output
         if (j > 0 && !(ok = warp_wait(&pv_done, (tile_no - 1) & 1, abort))) break;
@@ -714,30 +807,28 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
           }
         }
         unsigned char* p = smem + L::kPAt + row * 128;
+        const f2 by = pair_of(mulx, mulx), less = pair_of(-base, -base), minus = pair_of(-1.f, -1.f);
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 8) {
+        for (int c = 0; c < kKeys / 2; c += 4) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i0 = c + 2 * e, i1 = i0 + 1;
-            float p0 = ex2(fmaf(x[i0], mulx, -base)), p1 = ex2(fmaf(x[i1], mulx, -base));
-            l += p0;
-            l += p1;
+            float2 v = halves(fma2(x[c + e], by, less));
+            f2 w = pair_of(ex2(v.x), ex2(v.y));
+            l = sum2(l, w);
             if (FP32) {
-              const float2 v0 = *reinterpret_cast<const float2*>(&pairs[i0].z), v1 = *reinterpret_cast<const float2*>(&pairs[i1].z);
-              // a weight of zero (a masked row) takes nothing of its row, NaN included
-              z += p0 > 0.f ? p0 * v0.y : p0;
-              z += p1 > 0.f ? p1 * v1.y : p1;
-              p0 = p0 > 0.f ? p0 * (v0.x * unit) : p0;
-              p1 = p1 > 0.f ? p1 * (v1.x * unit) : p1;
+              z = fma2(w, *reinterpret_cast<const f2*>(pairs + 3 * kKeys + 2 * (c + e)), z);
+              w = mul2(w, *reinterpret_cast<const f2*>(pairs + 2 * kKeys + 2 * (c + e)));
             }
-            hi[e] = pack_half(p0, p1);
+            v = halves(w);
+            hi[e] = pack_half(v.x, v.y);
             if (FP32) {
               const float2 u = unpack_half(hi[e]);
-              lo[e] = pack_half(p0 - u.x, p1 - u.y);
+              v = halves(fma2(pair_of(u.x, u.y), minus, w));
+              lo[e] = pack_half(v.x, v.y);
             }
           }
-          unsigned char* at = p + (((c >> 3) ^ (row & 7)) << 4);
+          unsigned char* at = p + (((c >> 2) ^ (row & 7)) << 4);
           *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if (FP32) *reinterpret_cast<uint4*>(at + kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
@@ -753,7 +844,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       }
       // the output, or the run's partial
       const bool last = it.parts <= 1;
-      const float inv = last ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const float sum_l = halves(l).x + halves(l).y, sum_z = halves(z).x + halves(z).y;
+      const float inv = last ? (sum_l > 0.f || sum_l != sum_l ? 1.f / sum_l : 0.f) : 1.f;
       const float unit = FP32 ? pow2i(e_cur - 6) : 1.f;
       float* part = last ? nullptr : a.part + ((size_t)i * kQ + row) * (D + 4);
 #pragma unroll 1
@@ -768,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           if (FP32 && n > kFlush) o[e] += s[e];
-          o[e] = n > 0 ? (FP32 ? fmaf(o[e], unit, z) : o[e]) * inv : 0.f;
-          if (!FP32 && (nan_groups >> (c >> 6) & 1u)) o[e] = NAN;
+          o[e] = n > 0 ? (FP32 ? fmaf(o[e], unit, sum_z) : o[e]) * inv : 0.f;
+          if (nan_groups >> (c >> 6) & 1u) o[e] = NAN;
         }
         if (on) {
           float y0[8], y1[8];
@@ -791,9 +883,9 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       if (on) {
         if (!last) {
           part[D] = m;
-          part[D + 1] = l;
+          part[D + 1] = sum_l;
         } else if (a.lse != nullptr) {
-          a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = l > 0.f ? m + log2f(l) : INFINITY;
+          a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = sum_l > 0.f ? m + log2f(sum_l) : INFINITY;
         }
       }
       __syncwarp();
@@ -849,10 +941,10 @@ cudaError_t run(const PromptArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t kv4_prompt_partials(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
-  // whole query tiles below 2 x slots, their runs below 4 x slots (and none split otherwise)
+  // split tiles are fewer than 2 x slots, and have at most kMaxRounds x slots runs and one more each
   const long long tiles = ((long long)b.max_count * (g.nq / g.nkv) + kQ - 1) / kQ * g.nkv * b.n_seq;
   const long long runs = (b.max_rows + kKeys - 1) / kKeys / kMinRun + 1;
-  return (size_t)std::min<long long>(4ll * 2 * num_sms, tiles * runs) * kQ * (g.d + 4) * 4;
+  return (size_t)std::min<long long>((kMaxRounds + 2ll) * 2 * num_sms, tiles * runs) * kQ * (g.d + 4) * 4;
 }
 
 cudaError_t kv4_prompt(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4Attn& at, int least, float* part, float* lse, int num_sms,
