@@ -308,6 +308,18 @@ struct Raw {
   unsigned bad;
 };
 
+// Loads that stay where they are written: the compiler would move plain ones down to their use, a tile later.
+__device__ __forceinline__ uint32_t load_now(const uint32_t* p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint4 load_now(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
 template <int D>
 __device__ __forceinline__ void load_raw(Raw<D>& w, const PromptArgs& a, const uint8_t* b0, const uint8_t* b1, int t) {
   constexpr int kGroups = D / 64;
@@ -320,20 +332,20 @@ __device__ __forceinline__ void load_raw(Raw<D>& w, const PromptArgs& a, const u
     w.k[g] = make_uint4(0u, 0u, 0u, 0u);
     w.kp[g] = 0u;
     if (kb != nullptr) {
-      w.k[g] = __ldg(reinterpret_cast<const uint4*>(kb + kr * (D / 2) + g * 32 + (t & 1) * 16));
-      w.kp[g] = __ldg(reinterpret_cast<const uint32_t*>(kb + code_bytes(D) + (kr * kGroups + g) * 4));
+      w.k[g] = load_now(reinterpret_cast<const uint4*>(kb + kr * (D / 2) + g * 32 + (t & 1) * 16));
+      w.kp[g] = load_now(reinterpret_cast<const uint32_t*>(kb + code_bytes(D) + (kr * kGroups + g) * 4));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       w.v[g][i] = w.vp[g][i] = 0u;
       if (vb != nullptr) {
-        w.v[g][i] = __ldg(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + (vr + i) * (D / 2) + g * 32 + vw * 4));
-        w.vp[g][i] = __ldg(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + code_bytes(D) + ((vr + i) * kGroups + g) * 4));
+        w.v[g][i] = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + (vr + i) * (D / 2) + g * 32 + vw * 4));
+        w.vp[g][i] = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + code_bytes(D) + ((vr + i) * kGroups + g) * 4));
       }
     }
   }
   w.pos = 0;
-  if (a.g.track && (t & 1) == 0 && kb != nullptr) w.pos = __ldg(reinterpret_cast<const int*>(kb + pos_at(D) + 4 * kr));
+  if (a.g.track && (t & 1) == 0 && kb != nullptr) w.pos = (int)load_now(reinterpret_cast<const uint32_t*>(kb + pos_at(D) + 4 * kr));
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
@@ -518,22 +530,24 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
     // ------------------------------------------------------------ conversion and matrix instructions
     const int t = threadIdx.x - 128;
     bool ok = true;
-    const uint32_t sq_at = smem_of(smem + L::kQAt), sp_at = smem_of(smem + L::kPAt), k_at = smem_of(smem + L::kKAt), v_at = smem_of(smem + L::kVAt);
+    // descriptors of the operands' first tiles; 16 bytes on are 1 more
+    const uint64_t q_desc = tile_desc(smem_of(smem + L::kQAt)), p_desc = tile_desc(smem_of(smem + L::kPAt));
+    const uint64_t k_desc = tile_desc(smem_of(smem + L::kKAt)), v_desc = tile_desc(smem_of(smem + L::kVAt));
     unsigned items = 0;
     // (lane 0 of warp 4) S = Q K^T of key tile number `no`, the item's j-th
     auto score = [&](unsigned no, int j) {
       if (j == 0 && !mbar_wait(&q_full, items & 1, abort)) return false;
       if (!mbar_wait(&k_full[no & 1], (no >> 1) & 1, abort)) return false;
       fence_after();
-      const uint32_t kt = k_at + (no & 1) * L::kTile, d = tmem + (no & 1) * kKeys;
+      const uint64_t kd = k_desc + (no & 1) * (L::kTile / 16);
+      const uint32_t d = tmem + (no & 1) * kKeys;
 #pragma unroll
       for (int hf = 0; hf < L::kHalves; ++hf)
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma(d, tile_desc(sq_at + (hf * kGroups + g) * kQ * 128 + ks * 32), tile_desc(kt + g * kKeys * 128 + ks * 32), idesc(kKeys),
-                 hf + g + ks > 0 ? 1u : 0u);
+            umma(d, q_desc + (hf * kGroups + g) * (kQ * 8) + ks * 2, kd + g * (kKeys * 8) + ks * 2, idesc(kKeys), hf + g + ks > 0 ? 1u : 0u);
       umma_commit(&k_empty[no & 1]);
       umma_commit(&s_full[no & 1]);
       mbar_arrive(&s_full[no & 1]);  // and orders the conversion's notes before the softmax
@@ -544,13 +558,13 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       const int vs = L::kVStages == 2 ? no & 1 : 0;
       if (!mbar_wait(&v_full[vs], (no / L::kVStages) & 1, abort) || !mbar_wait(&p_full, no & 1, abort)) return false;
       fence_after();
-      const uint32_t vt = v_at + vs * L::kTile;
+      const uint64_t vd = v_desc + vs * (L::kTile / 16);
       const bool fresh = FP32 ? j % kFlush == 0 : j == 0;
 #pragma unroll
       for (int hf = 0; hf < L::kHalves; ++hf)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma(t_out, tile_desc(sp_at + hf * kQ * 128 + ks * 32), tile_desc(vt + ks * 32), idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
+          umma(t_out, p_desc + hf * (kQ * 8) + ks * 2, vd + ks * 2, idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
       umma_commit(&v_empty[vs]);
       umma_commit(&pv_done);
       return true;
@@ -683,103 +697,135 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
         const int st = tile_no & 1, slot = tile_no % kNotes, j = k - it.k0;
         if (!(ok = warp_wait(&s_full[st], (tile_no >> 1) & 1, abort))) break;
         fence_after();
-        f2 x[kKeys / 2];
-        tmem_ld32(tmem + lane_at + st * kKeys, x);
-        tmem_ld32(tmem + lane_at + st * kKeys + 32, x + 16);
-        tmem_wait_ld();
-        const float* pairs = reinterpret_cast<const float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
-        const unsigned bad = notes[slot].bad;
-        if (FP32) {
-          const f2 add = pair_of(addm, addm);
-#pragma unroll
-          for (int c = 0; c < kKeys / 2; c += 2) {
-            const ulonglong2 sk = *reinterpret_cast<const ulonglong2*>(pairs + 2 * c), zk = *reinterpret_cast<const ulonglong2*>(pairs + kKeys + 2 * c);
-            x[c] = fma2(sk.x, x[c], mul2(zk.x, add));
-            x[c + 1] = fma2(sk.y, x[c + 1], mul2(zk.y, add));
-          }
-        }
-        float mulx = mul;
-        if (FEAT) {
-          mulx = 1.f;
-          if (a.a.cap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap))
-            const f2 in = pair_of(mul * a.cap_in, mul * a.cap_in), one = pair_of(1.f, 1.f), out = pair_of(a.cap_out, a.cap_out),
-                     out2 = pair_of(-2.f * a.cap_out, -2.f * a.cap_out);
-#pragma unroll
-            for (int c = 0; c < kKeys / 2; ++c) {
-              float2 e = halves(mul2(x[c], in));
-              e = halves(sum2(pair_of(ex2(e.x), ex2(e.y)), one));
-              x[c] = fma2(pair_of(rcp(e.x), rcp(e.y)), out2, out);
-            }
-          } else {
-            const f2 by = pair_of(mul, mul);
-#pragma unroll
-            for (int c = 0; c < kKeys / 2; ++c) x[c] = mul2(x[c], by);
-          }
-          // distances, where there is a bias, or a window that leaves out some row of the tile for some query
-          if (a.a.slopes != nullptr || (a.a.window > 0 && (a.g.track || k * kKeys <= last_limit - a.a.window))) {
-            const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys;
-            const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
-#pragma unroll
-            for (int c = 0; c < kKeys / 2; ++c) {
-              float2 v = halves(x[c]);
-              const int g0 = (a.g.track ? pos[2 * c] : k * kKeys + 2 * c) - qpos, g1 = (a.g.track ? pos[2 * c + 1] : k * kKeys + 2 * c + 1) - qpos;
-              v.x = g0 <= win ? -INFINITY : fmaf(slope, (float)g0, v.x);
-              v.y = g1 <= win ? -INFINITY : fmaf(slope, (float)g1, v.y);
-              x[c] = pair_of(v.x, v.y);
-            }
-          }
-        }
-        if ((k + 1) * kKeys - 1 > first_limit || !whole_tile || bad != 0u) {
-#pragma unroll
-          for (int c = 0; c < kKeys / 2; ++c) {
-            float2 v = halves(x[c]);
-            const bool off = (bad >> (c >> 4)) & 1u;
-            if (off || k * kKeys + 2 * c > limit) v.x = -INFINITY;
-            if (off || k * kKeys + 2 * c + 1 > limit) v.y = -INFINITY;
-            x[c] = pair_of(v.x, v.y);
-          }
-        }
-        float top = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kKeys / 2; c += 2) {
-          const float2 v = halves(x[c]), u = halves(x[c + 1]);
-          top = fmaxf(top, fmaxf(v.x, v.y));
-          top1 = fmaxf(top1, fmaxf(u.x, u.y));
-        }
-        top = fmaxf(top, top1);
-        top = top == -INFINITY ? top : top * mulx;
-        float rescale = 1.f;
-        bool renew = top > m + kSlack;
-        int e_new = e_cur;
-        if (FP32) {
-          e_new = notes[slot].e;
-          renew = renew || e_new != e_cur;
-        }
-        const bool any = __any_sync(0xffffffffu, renew);
-        if (any) {
-          const float nm = fmaxf(m, top);
-          rescale = nm == -INFINITY ? 1.f : ex2(m - nm);
-          m = nm;
-          l = mul2(l, pair_of(rescale, rescale));
-          z = mul2(z, pair_of(rescale, rescale));
-          if (FP32) rescale *= pow2i(e_cur - e_new);
-          e_cur = e_new;
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        if ((notes[slot].nan[0] | notes[slot].nan[1]) != 0ull) {
-          // rows of V that are NaN: the output of those who see them is NaN
-          const unsigned long long n0 = notes[slot].nan[0], n1 = notes[slot].nan[1];
-#pragma unroll
-          for (int c = 0; c < kKeys / 2; ++c) {
-            const float2 v = halves(x[c]);
-            const unsigned b0 = (unsigned)(n0 >> (2 * c)) & 3u, b1 = (unsigned)(n1 >> (2 * c)) & 3u;
-            if (!(v.x == -INFINITY)) nan_groups |= (b0 & 1u) | (b1 & 1u) << 1;
-            if (!(v.y == -INFINITY)) nan_groups |= (b0 >> 1) | (b1 & 2u);
-          }
-        }
         // the product before has read the weights and left the output
         if (j > 0 && !(ok = warp_wait(&pv_done, (tile_no - 1) & 1, abort))) break;
         fence_after();
+        const float* pairs = reinterpret_cast<const float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
+        const TileNote note = notes[slot];
+        const bool masked = (k + 1) * kKeys - 1 > first_limit || !whole_tile || note.bad != 0u;
+        // distances, where there is a bias, or a window that leaves out some row of the tile for some query
+        const bool gaps = FEAT && (a.a.slopes != nullptr || (a.a.window > 0 && (a.g.track || k * kKeys <= last_limit - a.a.window)));
+        // One pass over the scores, 32 at a time: the weights relative to the present maximum, to shared memory.  Returns
+        // the largest score; where it exceeds the maximum by 2^kSlack, the pass is made again with the new one.
+        auto pass = [&](float base) {
+          const f2 by = FEAT ? pair_of(1.f, 1.f) : pair_of(mul, mul), less = pair_of(-base, -base), minus = pair_of(-1.f, -1.f);
+          float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 32) {
+            f2 x[16];
+            tmem_ld32(tmem + lane_at + st * kKeys + c0, x);
+            tmem_wait_ld();
+            if (FP32) {
+              const f2 add = pair_of(addm, addm);
+#pragma unroll
+              for (int c = 0; c < 16; c += 2) {
+                const ulonglong2 sk = *reinterpret_cast<const ulonglong2*>(pairs + c0 + 2 * c);
+                const ulonglong2 zk = *reinterpret_cast<const ulonglong2*>(pairs + kKeys + c0 + 2 * c);
+                x[c] = fma2(sk.x, x[c], mul2(zk.x, add));
+                x[c + 1] = fma2(sk.y, x[c + 1], mul2(zk.y, add));
+              }
+            }
+            if (FEAT) {
+              if (a.a.cap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap))
+                const f2 in = pair_of(mul * a.cap_in, mul * a.cap_in), one = pair_of(1.f, 1.f), out = pair_of(a.cap_out, a.cap_out),
+                         out2 = pair_of(-2.f * a.cap_out, -2.f * a.cap_out);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  float2 e = halves(mul2(x[c], in));
+                  e = halves(sum2(pair_of(ex2(e.x), ex2(e.y)), one));
+                  x[c] = fma2(pair_of(rcp(e.x), rcp(e.y)), out2, out);
+                }
+              } else {
+                const f2 all = pair_of(mul, mul);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) x[c] = mul2(x[c], all);
+              }
+              if (gaps) {
+                const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys + c0;
+                const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  float2 v = halves(x[c]);
+                  const int at = k * kKeys + c0 + 2 * c;
+                  const int g0 = (a.g.track ? pos[2 * c] : at) - qpos, g1 = (a.g.track ? pos[2 * c + 1] : at + 1) - qpos;
+                  v.x = g0 <= win ? -INFINITY : fmaf(slope, (float)g0, v.x);
+                  v.y = g1 <= win ? -INFINITY : fmaf(slope, (float)g1, v.y);
+                  x[c] = pair_of(v.x, v.y);
+                }
+              }
+            }
+            if (masked) {
+              const int lim = (note.bad >> (c0 >> 5)) & 1u ? -1 : limit;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                float2 v = halves(x[c]);
+                const int at = k * kKeys + c0 + 2 * c;
+                x[c] = pair_of(at > lim ? -INFINITY : v.x, at + 1 > lim ? -INFINITY : v.y);
+              }
+            }
+            if ((note.nan[0] | note.nan[1]) != 0ull) {
+              // rows of V that are NaN: the output of those who see them is NaN
+              const unsigned n0 = (unsigned)(note.nan[0] >> c0), n1 = (unsigned)(note.nan[1] >> c0);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float2 v = halves(x[c]);
+                const unsigned b0 = n0 >> (2 * c), b1 = n1 >> (2 * c);
+                if (!(v.x == -INFINITY)) nan_groups |= (b0 & 1u) | (b1 & 1u) << 1;
+                if (!(v.y == -INFINITY)) nan_groups |= (b0 >> 1 & 1u) | (b1 & 2u);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const float2 v = halves(x[c]), u = halves(x[c + 1]);
+              top = fmaxf(top, fmaxf(v.x, v.y));
+              top1 = fmaxf(top1, fmaxf(u.x, u.y));
+            }
+            unsigned char* p = smem + L::kPAt + row * 128;
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float2 v = halves(fma2(x[c + e], by, less));
+                f2 w = pair_of(ex2(v.x), ex2(v.y));
+                l = sum2(l, w);
+                if (FP32) {
+                  z = fma2(w, *reinterpret_cast<const f2*>(pairs + 3 * kKeys + c0 + 2 * (c + e)), z);
+                  w = mul2(w, *reinterpret_cast<const f2*>(pairs + 2 * kKeys + c0 + 2 * (c + e)));
+                }
+                v = halves(w);
+                hi[e] = pack_half(v.x, v.y);
+                if (FP32) {
+                  const float2 u = unpack_half(hi[e]);
+                  v = halves(fma2(pair_of(u.x, u.y), minus, w));
+                  lo[e] = pack_half(v.x, v.y);
+                }
+              }
+              unsigned char* at = p + ((((c0 + 2 * c) >> 3) ^ (row & 7)) << 4);
+              *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              if (FP32) *reinterpret_cast<uint4*>(at + kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+          top = fmaxf(top, top1);
+          return FEAT || top == -INFINITY ? top : top * mul;
+        };
+        const f2 l_before = l, z_before = z;
+        const float top = pass(m == -INFINITY ? 0.f : m);
+        float rescale = 1.f;
+        const bool again = __any_sync(0xffffffffu, top > m + kSlack);
+        if (again) {
+          const float nm = fmaxf(m, top);
+          rescale = nm == -INFINITY ? 1.f : ex2(m - nm);
+          m = nm;
+          l = mul2(l_before, pair_of(rescale, rescale));
+          z = mul2(z_before, pair_of(rescale, rescale));
+          pass(m == -INFINITY ? 0.f : m);
+        }
+        const bool any = again || (FP32 && note.e != e_cur);
+        if (FP32) {
+          rescale *= pow2i(e_cur - note.e);
+          e_cur = note.e;
+        }
         if (j > 0) {
           if (FP32 && j % kFlush == 0) {  // move the output to the sums
 #pragma unroll 1
@@ -805,32 +851,6 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
             }
             tmem_wait_st();
           }
-        }
-        unsigned char* p = smem + L::kPAt + row * 128;
-        const f2 by = pair_of(mulx, mulx), less = pair_of(-base, -base), minus = pair_of(-1.f, -1.f);
-#pragma unroll
-        for (int c = 0; c < kKeys / 2; c += 4) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 v = halves(fma2(x[c + e], by, less));
-            f2 w = pair_of(ex2(v.x), ex2(v.y));
-            l = sum2(l, w);
-            if (FP32) {
-              z = fma2(w, *reinterpret_cast<const f2*>(pairs + 3 * kKeys + 2 * (c + e)), z);
-              w = mul2(w, *reinterpret_cast<const f2*>(pairs + 2 * kKeys + 2 * (c + e)));
-            }
-            v = halves(w);
-            hi[e] = pack_half(v.x, v.y);
-            if (FP32) {
-              const float2 u = unpack_half(hi[e]);
-              v = halves(fma2(pair_of(u.x, u.y), minus, w));
-              lo[e] = pack_half(v.x, v.y);
-            }
-          }
-          unsigned char* at = p + (((c >> 2) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (FP32) *reinterpret_cast<uint4*>(at + kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_async();
         fence_before();
