@@ -4,10 +4,10 @@
 // A CTA takes 128 query rows -- (token, query head) pairs that read one KV head -- through a run of key tiles
 // of 64 cache rows.  Warps 4 .. 7 turn the rows into fp16 operands in shared memory (128-byte swizzle, K as
 // [row][dim], V as [dim][row]), a lane of warp 4 issues the matrix instructions in between (a warp of its own would
-// cost all the others 32 registers), and thread i of warps 0 .. 3 owns query row i: it reads the row's scores from tensor memory, keeps its softmax and writes its
-// weights as the second product's operand.  Scores have two buffers in tensor memory and K two stages, so that the
-// tensor cores and the conversion work one tile ahead of the softmax; two CTAs share an SM, so that one's softmax
-// fills the other's waits (for which head dim 128 leaves V one stage).
+// cost all the others 32 registers), and thread i of warps 0 .. 3 owns query row i: it reads the row's scores from
+// tensor memory, keeps its softmax and writes its weights over the scores, where the second product takes them
+// from.  Scores have two buffers and K and V two stages, so that the tensor cores and the conversion work one tile
+// ahead of the softmax; two CTAs share an SM, so that one's softmax fills the other's waits.
 //   bf16: K and V are the values lo + scale * code rounded to fp16 (one rounding, 2^-11; bf16 has 2^-8),
 // the weights are rounded to fp16 too.
 //   fp32 (head dim 64): the operands are code - 8, exact; q and the weights are hi + lo fp16 (22 bits); the
@@ -49,7 +49,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, unsigned parity) {
   return ok != 0;
 }
 // Waits for the phase of the given parity; false after kWaitNs, or once another thread has given up.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* b, unsigned parity, volatile unsigned* failed) {
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t* b, unsigned parity, volatile unsigned* failed) {
   unsigned long long t0 = 0ull;
   for (unsigned spins = 0;; ++spins) {
     if (mbar_test(b, parity)) return true;
@@ -80,6 +80,12 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
 }
 __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a),
+               "l"(b), "r"(desc), "r"(accumulate)
+               : "memory");
+}
+// The same with the first operand in tensor memory: a row a lane, two fp16 a column.
+__device__ __forceinline__ void umma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a),
                "l"(b), "r"(desc), "r"(accumulate)
                : "memory");
 }
@@ -148,6 +154,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at), "r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
+      "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
@@ -164,11 +177,9 @@ template <int D, bool FP32>
 struct Layout {
   static constexpr int kGroups = D / 64, kHalves = FP32 ? 2 : 1;
   static constexpr int kQBytes = kQ * 128 * kGroups * kHalves;  // per half and group: [128][64] fp16
-  static constexpr int kPBytes = kQ * 128 * kHalves;
   static constexpr int kTile = kKeys * 128 * kGroups;           // K: per group [64 rows][64 dims]; V: [D dims][64 rows]
-  static constexpr int kVStages = D == 64 ? 2 : 1;
-  static constexpr int kQAt = 0, kPAt = kQBytes, kKAt = kPAt + kPBytes, kVAt = kKAt + 2 * kTile;
-  static constexpr int kPairsAt = kVAt + kVStages * kTile;      // fp32: float [kNotes][4: sk, zk, sv, zv][64]
+  static constexpr int kQAt = 0, kKAt = kQBytes, kVAt = kKAt + 2 * kTile;
+  static constexpr int kPairsAt = kVAt + 2 * kTile;             // fp32: float [kNotes][4: sk, zk, sv, zv][64]
   static constexpr int kPosAt = kPairsAt + (FP32 ? kNotes * kKeys * 16 : 0);
   static constexpr int kInfoAt = kPosAt + kNotes * kKeys * 4;   // then SeqInfo [n_seq]
 };
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
   using L = Layout<D, FP32>;
   constexpr int kGroups = D / 64;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, pv_done, q_full, drain;
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], pv_done[2], p_full, q_full, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ unsigned failed;
   __shared__ TileNote notes[kNotes];
@@ -504,10 +515,10 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       mbar_init(&v_full[i], 128);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 2);
+      mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drain, 1);
     mbar_init(&p_full, 128);
-    mbar_init(&pv_done, 1);
     mbar_init(&q_full, 128);
     failed = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -528,10 +539,11 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
 
   if (warp >= 4) {
     // ------------------------------------------------------------ conversion and matrix instructions
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");  // of 128 at launch; the softmax takes them
     const int t = threadIdx.x - 128;
     bool ok = true;
     // descriptors of the operands' first tiles; 16 bytes on are 1 more
-    const uint64_t q_desc = tile_desc(smem_of(smem + L::kQAt)), p_desc = tile_desc(smem_of(smem + L::kPAt));
+    const uint64_t q_desc = tile_desc(smem_of(smem + L::kQAt));
     const uint64_t k_desc = tile_desc(smem_of(smem + L::kKAt)), v_desc = tile_desc(smem_of(smem + L::kVAt));
     unsigned items = 0;
     // (lane 0 of warp 4) S = Q K^T of key tile number `no`, the item's j-th
@@ -555,18 +567,18 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
     };
     // (the same lane) O += P V
     auto product = [&](unsigned no, int j) {
-      const int vs = L::kVStages == 2 ? no & 1 : 0;
-      if (!mbar_wait(&v_full[vs], (no / L::kVStages) & 1, abort) || !mbar_wait(&p_full, no & 1, abort)) return false;
+      const int st = no & 1;
+      if (!mbar_wait(&v_full[st], (no >> 1) & 1, abort) || !mbar_wait(&p_full, no & 1, abort)) return false;
       fence_after();
-      const uint64_t vd = v_desc + vs * (L::kTile / 16);
+      const uint64_t vd = v_desc + st * (L::kTile / 16);
       const bool fresh = FP32 ? j % kFlush == 0 : j == 0;
 #pragma unroll
       for (int hf = 0; hf < L::kHalves; ++hf)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma(t_out, p_desc + hf * (kQ * 8) + ks * 2, vd + ks * 2, idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
-      umma_commit(&v_empty[vs]);
-      umma_commit(&pv_done);
+        for (int ks = 0; ks < 4; ++ks)  // 32 keys' weights, hi and lo, lie in the 32 columns of their scores
+          umma_tmem(t_out, tmem + st * kKeys + (ks >> 1) * 32 + hf * 16 + (ks & 1) * 8, vd + ks * 2, idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
+      umma_commit(&v_empty[st]);
+      umma_commit(&pv_done[st]);
       return true;
     };
     for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
@@ -600,25 +612,18 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
           p0 = page(r + kKeys);
           p1 = page(r + kKeys + kRows);
         }
-        const int st = tile_no & 1, vs = L::kVStages == 2 ? st : 0, slot = tile_no % kNotes;
-        const unsigned vn = tile_no / L::kVStages;  // how often V's stage was used before
+        const int st = tile_no & 1, slot = tile_no % kNotes;
         cur.bad &= k * kKeys + kRows < sq.r ? 3u : 1u;  // a block behind the cache's end has no page: not an error
         if (tile_no >= 2 && !(ok = warp_wait(&k_empty[st], ((tile_no >> 1) - 1) & 1, abort))) break;
         convert_k<D, FP32>(cur, a, smem + L::kKAt + st * L::kTile, smem, slot, k * kKeys, sq.r, t, &notes[slot], &e_run);
         fence_async();
         mbar_arrive(&k_full[st]);
-        auto value = [&] {
-          if (vn >= 1 && !warp_wait(&v_empty[vs], (vn - 1) & 1, abort)) return false;
-          convert_v<D, FP32>(cur, smem + L::kVAt + vs * L::kTile, k * kKeys, sq.r, t);
-          fence_async();
-          mbar_arrive(&v_full[vs]);
-          return true;
-        };
-        // with one stage of V the product before has to be under way before V's turn comes
-        if (L::kVStages == 2 && !(ok = value())) break;
+        if (tile_no >= 2 && !(ok = warp_wait(&v_empty[st], ((tile_no >> 1) - 1) & 1, abort))) break;
+        convert_v<D, FP32>(cur, smem + L::kVAt + st * L::kTile, k * kKeys, sq.r, t);
+        fence_async();
+        mbar_arrive(&v_full[st]);
         if (t == 0) ok = score(tile_no, k - it.k0) && (k == it.k0 || product(tile_no - 1, k - it.k0 - 1));
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (L::kVStages == 1 && !(ok = value())) break;
         cur = nxt;
       }
       if (ok && t == 0) ok = product(tile_no - 1, it.k1 - it.k0 - 1);
@@ -627,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
     }
   } else {
     // ------------------------------------------------------------ softmax: one query row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     const int row = threadIdx.x;
     const uint32_t lane_at = (uint32_t)(warp * 32) << 16;
     bool ok = true;
@@ -697,137 +703,94 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
         const int st = tile_no & 1, slot = tile_no % kNotes, j = k - it.k0;
         if (!(ok = warp_wait(&s_full[st], (tile_no >> 1) & 1, abort))) break;
         fence_after();
-        // the product before has read the weights and left the output
-        if (j > 0 && !(ok = warp_wait(&pv_done, (tile_no - 1) & 1, abort))) break;
-        fence_after();
+        f2 x[kKeys / 2];
+        tmem_ld32(tmem + lane_at + st * kKeys, x);
+        tmem_ld32(tmem + lane_at + st * kKeys + 32, x + 16);
         const float* pairs = reinterpret_cast<const float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
         const TileNote note = notes[slot];
-        const bool masked = (k + 1) * kKeys - 1 > first_limit || !whole_tile || note.bad != 0u;
-        // distances, where there is a bias, or a window that leaves out some row of the tile for some query
-        const bool gaps = FEAT && (a.a.slopes != nullptr || (a.a.window > 0 && (a.g.track || k * kKeys <= last_limit - a.a.window)));
-        // One pass over the scores, 32 at a time: the weights relative to the present maximum, to shared memory.  Returns
-        // the largest score; where it exceeds the maximum by 2^kSlack, the pass is made again with the new one.
-        auto pass = [&](float base) {
-          const f2 by = FEAT ? pair_of(1.f, 1.f) : pair_of(mul, mul), less = pair_of(-base, -base), minus = pair_of(-1.f, -1.f);
-          float top = -INFINITY, top1 = -INFINITY;
-#pragma unroll 1
-          for (int c0 = 0; c0 < kKeys; c0 += 32) {
-            f2 x[16];
-            tmem_ld32(tmem + lane_at + st * kKeys + c0, x);
-            tmem_wait_ld();
-            if (FP32) {
-              const f2 add = pair_of(addm, addm);
+        tmem_wait_ld();
+        if (FP32) {
+          const f2 add = pair_of(addm, addm);
 #pragma unroll
-              for (int c = 0; c < 16; c += 2) {
-                const ulonglong2 sk = *reinterpret_cast<const ulonglong2*>(pairs + c0 + 2 * c);
-                const ulonglong2 zk = *reinterpret_cast<const ulonglong2*>(pairs + kKeys + c0 + 2 * c);
-                x[c] = fma2(sk.x, x[c], mul2(zk.x, add));
-                x[c + 1] = fma2(sk.y, x[c + 1], mul2(zk.y, add));
-              }
+          for (int c = 0; c < kKeys / 2; c += 2) {
+            const ulonglong2 sk = *reinterpret_cast<const ulonglong2*>(pairs + 2 * c), zk = *reinterpret_cast<const ulonglong2*>(pairs + kKeys + 2 * c);
+            x[c] = fma2(sk.x, x[c], mul2(zk.x, add));
+            x[c + 1] = fma2(sk.y, x[c + 1], mul2(zk.y, add));
+          }
+        }
+        if (FEAT) {
+          if (a.a.cap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap))
+            const f2 in = pair_of(mul * a.cap_in, mul * a.cap_in), one = pair_of(1.f, 1.f), out = pair_of(a.cap_out, a.cap_out),
+                     out2 = pair_of(-2.f * a.cap_out, -2.f * a.cap_out);
+#pragma unroll
+            for (int c = 0; c < kKeys / 2; ++c) {
+              float2 e = halves(mul2(x[c], in));
+              e = halves(sum2(pair_of(ex2(e.x), ex2(e.y)), one));
+              x[c] = fma2(pair_of(rcp(e.x), rcp(e.y)), out2, out);
             }
-            if (FEAT) {
-              if (a.a.cap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap))
-                const f2 in = pair_of(mul * a.cap_in, mul * a.cap_in), one = pair_of(1.f, 1.f), out = pair_of(a.cap_out, a.cap_out),
-                         out2 = pair_of(-2.f * a.cap_out, -2.f * a.cap_out);
+          } else {
+            const f2 all = pair_of(mul, mul);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  float2 e = halves(mul2(x[c], in));
-                  e = halves(sum2(pair_of(ex2(e.x), ex2(e.y)), one));
-                  x[c] = fma2(pair_of(rcp(e.x), rcp(e.y)), out2, out);
-                }
-              } else {
-                const f2 all = pair_of(mul, mul);
+            for (int c = 0; c < kKeys / 2; ++c) x[c] = mul2(x[c], all);
+          }
+          // distances, where there is a bias, or a window that leaves out some row of the tile for some query
+          if (a.a.slopes != nullptr || (a.a.window > 0 && (a.g.track || k * kKeys <= last_limit - a.a.window))) {
+            const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys;
+            const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) x[c] = mul2(x[c], all);
-              }
-              if (gaps) {
-                const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys + c0;
-                const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  float2 v = halves(x[c]);
-                  const int at = k * kKeys + c0 + 2 * c;
-                  const int g0 = (a.g.track ? pos[2 * c] : at) - qpos, g1 = (a.g.track ? pos[2 * c + 1] : at + 1) - qpos;
-                  v.x = g0 <= win ? -INFINITY : fmaf(slope, (float)g0, v.x);
-                  v.y = g1 <= win ? -INFINITY : fmaf(slope, (float)g1, v.y);
-                  x[c] = pair_of(v.x, v.y);
-                }
-              }
-            }
-            if (masked) {
-              const int lim = (note.bad >> (c0 >> 5)) & 1u ? -1 : limit;
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                float2 v = halves(x[c]);
-                const int at = k * kKeys + c0 + 2 * c;
-                x[c] = pair_of(at > lim ? -INFINITY : v.x, at + 1 > lim ? -INFINITY : v.y);
-              }
-            }
-            if ((note.nan[0] | note.nan[1]) != 0ull) {
-              // rows of V that are NaN: the output of those who see them is NaN
-              const unsigned n0 = (unsigned)(note.nan[0] >> c0), n1 = (unsigned)(note.nan[1] >> c0);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float2 v = halves(x[c]);
-                const unsigned b0 = n0 >> (2 * c), b1 = n1 >> (2 * c);
-                if (!(v.x == -INFINITY)) nan_groups |= (b0 & 1u) | (b1 & 1u) << 1;
-                if (!(v.y == -INFINITY)) nan_groups |= (b0 >> 1 & 1u) | (b1 & 2u);
-              }
-            }
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              const float2 v = halves(x[c]), u = halves(x[c + 1]);
-              top = fmaxf(top, fmaxf(v.x, v.y));
-              top1 = fmaxf(top1, fmaxf(u.x, u.y));
-            }
-            unsigned char* p = smem + L::kPAt + row * 128;
-#pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float2 v = halves(fma2(x[c + e], by, less));
-                f2 w = pair_of(ex2(v.x), ex2(v.y));
-                l = sum2(l, w);
-                if (FP32) {
-                  z = fma2(w, *reinterpret_cast<const f2*>(pairs + 3 * kKeys + c0 + 2 * (c + e)), z);
-                  w = mul2(w, *reinterpret_cast<const f2*>(pairs + 2 * kKeys + c0 + 2 * (c + e)));
-                }
-                v = halves(w);
-                hi[e] = pack_half(v.x, v.y);
-                if (FP32) {
-                  const float2 u = unpack_half(hi[e]);
-                  v = halves(fma2(pair_of(u.x, u.y), minus, w));
-                  lo[e] = pack_half(v.x, v.y);
-                }
-              }
-              unsigned char* at = p + ((((c0 + 2 * c) >> 3) ^ (row & 7)) << 4);
-              *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              if (FP32) *reinterpret_cast<uint4*>(at + kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int c = 0; c < kKeys / 2; ++c) {
+              float2 v = halves(x[c]);
+              const int at = k * kKeys + 2 * c;
+              const int g0 = (a.g.track ? pos[2 * c] : at) - qpos, g1 = (a.g.track ? pos[2 * c + 1] : at + 1) - qpos;
+              v.x = g0 <= win ? -INFINITY : fmaf(slope, (float)g0, v.x);
+              v.y = g1 <= win ? -INFINITY : fmaf(slope, (float)g1, v.y);
+              x[c] = pair_of(v.x, v.y);
             }
           }
-          top = fmaxf(top, top1);
-          return FEAT || top == -INFINITY ? top : top * mul;
-        };
-        const f2 l_before = l, z_before = z;
-        const float top = pass(m == -INFINITY ? 0.f : m);
+        }
+        if ((k + 1) * kKeys - 1 > first_limit || !whole_tile || note.bad != 0u) {
+#pragma unroll
+          for (int c = 0; c < kKeys / 2; ++c) {
+            const int lim = (note.bad >> (c >> 4)) & 1u ? -1 : limit, at = k * kKeys + 2 * c;
+            const float2 v = halves(x[c]);
+            x[c] = pair_of(at > lim ? -INFINITY : v.x, at + 1 > lim ? -INFINITY : v.y);
+          }
+        }
+        if ((note.nan[0] | note.nan[1]) != 0ull) {
+          // rows of V that are NaN: the output of those who see them is NaN
+#pragma unroll
+          for (int c = 0; c < kKeys / 2; ++c) {
+            const float2 v = halves(x[c]);
+            const unsigned b0 = (unsigned)(note.nan[0] >> (2 * c)), b1 = (unsigned)(note.nan[1] >> (2 * c));
+            if (!(v.x == -INFINITY)) nan_groups |= (b0 & 1u) | (b1 & 1u) << 1;
+            if (!(v.y == -INFINITY)) nan_groups |= (b0 >> 1 & 1u) | (b1 & 2u);
+          }
+        }
+        float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; c += 2) {
+          const float2 v = halves(x[c]), u = halves(x[c + 1]);
+          top = fmaxf(top, fmaxf(v.x, v.y));
+          top1 = fmaxf(top1, fmaxf(u.x, u.y));
+        }
+        top = fmaxf(top, top1);
+        top = FEAT || top == -INFINITY ? top : top * mul;
+        const bool renew = __any_sync(0xffffffffu, top > m + kSlack) || (FP32 && note.e != e_cur), flush = FP32 && j > 0 && j % kFlush == 0;
         float rescale = 1.f;
-        const bool again = __any_sync(0xffffffffu, top > m + kSlack);
-        if (again) {
+        if (renew) {
           const float nm = fmaxf(m, top);
           rescale = nm == -INFINITY ? 1.f : ex2(m - nm);
           m = nm;
-          l = mul2(l_before, pair_of(rescale, rescale));
-          z = mul2(z_before, pair_of(rescale, rescale));
-          pass(m == -INFINITY ? 0.f : m);
-        }
-        const bool any = again || (FP32 && note.e != e_cur);
-        if (FP32) {
-          rescale *= pow2i(e_cur - note.e);
+          l = mul2(l, pair_of(rescale, rescale));
+          z = mul2(z, pair_of(rescale, rescale));
+          if (FP32) rescale *= pow2i(e_cur - note.e);
           e_cur = note.e;
         }
-        if (j > 0) {
-          if (FP32 && j % kFlush == 0) {  // move the output to the sums
+        if (j > 0 && (renew || flush)) {
+          // the output, once the product before has left it
+          if (!(ok = warp_wait(&pv_done[st ^ 1], ((tile_no - 1) >> 1) & 1, abort))) break;
+          fence_after();
+          if (flush) {  // moved to the sums
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
               float o[16], s[16];
@@ -838,8 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
               for (int e = 0; e < 16; ++e) o[e] = (j > kFlush ? o[e] + s[e] : o[e]) * rescale;
               tmem_st16(t_sum + lane_at + c, o);
             }
-            tmem_wait_st();
-          } else if (any) {
+          } else {
 #pragma unroll 1
             for (int c = 0; c < (FP32 && j > kFlush ? 128 : D); c += 16) {
               float o[16];
@@ -849,17 +811,42 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
               for (int e = 0; e < 16; ++e) o[e] *= rescale;
               tmem_st16(t_out + lane_at + c, o);
             }
-            tmem_wait_st();
           }
         }
-        fence_async();
+        // the weights, 32 keys at a time over their own scores: 16 columns of hi, fp32: 16 of lo
+        const float base = m == -INFINITY ? 0.f : m;
+        const f2 by = FEAT ? pair_of(1.f, 1.f) : pair_of(mul, mul), less = pair_of(-base, -base), minus = pair_of(-1.f, -1.f);
+#pragma unroll
+        for (int c0 = 0; c0 < kKeys / 2; c0 += 16) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float2 v = halves(fma2(x[c0 + c], by, less));
+            f2 w = pair_of(ex2(v.x), ex2(v.y));
+            l = sum2(l, w);
+            if (FP32) {
+              z = fma2(w, *reinterpret_cast<const f2*>(pairs + 3 * kKeys + 2 * (c0 + c)), z);
+              w = mul2(w, *reinterpret_cast<const f2*>(pairs + 2 * kKeys + 2 * (c0 + c)));
+            }
+            v = halves(w);
+            hi[c] = pack_half(v.x, v.y);
+            if (FP32) {
+              const float2 u = unpack_half(hi[c]);
+              v = halves(fma2(pair_of(u.x, u.y), minus, w));
+              lo[c] = pack_half(v.x, v.y);
+            }
+          }
+          tmem_st16(tmem + lane_at + st * kKeys + 2 * c0, hi);
+          if (FP32) tmem_st16(tmem + lane_at + st * kKeys + 2 * c0 + 16, lo);
+        }
+        tmem_wait_st();
         fence_before();
         mbar_arrive(&p_full);
       }
       if (!ok) break;
       const int n = it.k1 - it.k0;
       if (n > 0) {
-        if (!(ok = warp_wait(&pv_done, (tile_no - 1) & 1, abort))) break;
+        if (!(ok = warp_wait(&pv_done[(tile_no - 1) & 1], ((tile_no - 1) >> 1) & 1, abort))) break;
         fence_after();
       }
       // the output, or the run's partial
