@@ -1,13 +1,14 @@
 // mbk_kv4_prompt.cu -- attention of many query rows (prompts, chunks of prompts) over the 4-bit KV cache, on
 // tcgen05.
 //
-// A CTA takes 128 query rows -- (token, query head) pairs that read one KV head -- through a run of key tiles
-// of 64 cache rows.  Warps 4 .. 7 turn the rows into fp16 operands in shared memory (128-byte swizzle, K as
-// [row][dim], V as [dim][row]), a lane of warp 4 issues the matrix instructions in between (a warp of its own would
-// cost all the others 32 registers), and thread i of warps 0 .. 3 owns query row i: it reads the row's scores from
+// A CTA takes 256 query rows -- (token, query head) pairs that read one KV head -- as two tiles of 128 through a run
+// of key tiles of 64 cache rows.  Four warps turn K's rows into fp16 operands in shared memory (128-byte
+// swizzle, [row][dim]) and four V's ([dim][row]), once for both query tiles; a lane of the first issues the matrix
+// instructions in between; and a thread of the other eight warps owns a query row: it reads the row's scores from
 // tensor memory, keeps its softmax and writes its weights over the scores, where the second product takes them
-// from.  Scores have two buffers and K and V two stages, so that the tensor cores and the conversion work one tile
-// ahead of the softmax; two CTAs share an SM, so that one's softmax fills the other's waits.
+// from.  Scores have two buffers and K and V two stages, so that conversion and tensor cores work one tile
+// ahead of the softmax.  (Two CTAs of one query tile and four conversion warps each were slower, 400 us against the
+// time in the table: the conversion held the softmax up.)
 //   bf16: K and V are the values lo + scale * code rounded to fp16 (one rounding, 2^-11; bf16 has 2^-8),
 // the weights are rounded to fp16 too.
 //   fp32 (head dim 64): the operands are code - 8, exact; q and the weights are hi + lo fp16 (22 bits); the
@@ -21,9 +22,10 @@ namespace mbk {
 namespace {
 
 constexpr int kQ = 128;        // query rows of a tile: tensor-memory lanes
+constexpr int kItem = 256;     // query rows of an item: two tiles
 constexpr int kKeys = 64;      // cache rows of a key tile: one 128-byte row of fp16
-constexpr int kThreads = 256;  // softmax 128, conversion 128
-constexpr int kTmemCols = 256; // scores 2 x 64, output 64 or 128, fp32: sums 64
+constexpr int kThreads = 512;  // softmax 2 x 128, K 128, V 128
+constexpr int kTmemCols = 512; // per query tile: scores 2 x 64, output 64 or 128, fp32: sums 64
 constexpr int kFlush = 8;      // fp32: tiles between two moves of the output
 constexpr int kMaxRounds = 4;  // items per CTA at most, about, where keys are split
 constexpr int kNotes = 4;      // tiles whose notes and pairs are kept
@@ -91,6 +93,13 @@ __device__ __forceinline__ void umma_tmem(uint32_t d, uint32_t a, uint64_t b, ui
 }
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+// One lane of a converged warp, always the same one.  The matrix instructions take their operands from uniform registers;
+// in a branch on a thread index the compiler would move each of them there, one by one (85 clocks an instruction).
+__device__ __forceinline__ bool elected() {
+  unsigned p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0u;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -172,11 +181,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
 // The shared memory of a CTA.
 template <int D, bool FP32>
 struct Layout {
   static constexpr int kGroups = D / 64, kHalves = FP32 ? 2 : 1;
-  static constexpr int kQBytes = kQ * 128 * kGroups * kHalves;  // per half and group: [128][64] fp16
+  static constexpr int kQTile = kQ * 128 * kGroups * kHalves;   // per half and group: [128][64] fp16
+  static constexpr int kQBytes = 2 * kQTile;
   static constexpr int kTile = kKeys * 128 * kGroups;           // K: per group [64 rows][64 dims]; V: [D dims][64 rows]
   static constexpr int kQAt = 0, kKAt = kQBytes, kVAt = kKAt + 2 * kTile;
   static constexpr int kPairsAt = kVAt + 2 * kTile;             // fp32: float [kNotes][4: sk, zk, sv, zv][64]
@@ -187,28 +202,28 @@ struct Layout {
 // What the conversion tells the softmax about a tile.  Written with K, at most two tiles ahead of the scores, which are
 // one ahead of the softmax: four slots.
 struct TileNote {
-  unsigned bad;                // bit b: block b of the tile lies in a page outside the pool
-  int e;                       // fp32: exponent of the largest scale of V so far
-  unsigned long long nan[2];   // rows whose V is NaN, per group of 64 dims (they are zero for the products)
+  unsigned bad;        // bit b: block b of the tile lies in a page outside the pool
+  int e[2];            // fp32: exponent of the largest scale of V, per 32 rows
+  unsigned nan[2][2];  // rows whose V is NaN, per group of 64 dims and 32 rows (they are zero for the products)
 };
 
 // ---------------------------------------------------------------- work items
-// An item is (sequence, KV head, 128 query rows, run of at most kt key tiles).  Items go round the CTAs, the
+// An item is (sequence, KV head, 256 query rows, run of at most kt key tiles).  Items go round the CTAs, the
 // tiles with most keys first.
 struct Work {
   int n_seq, nkv, grp, window, track, kt, total;
   const SeqInfo* seq;
-  __device__ int tiles(const SeqInfo& q) const { return (q.c * grp + kQ - 1) / kQ; }
+  __device__ int tiles(const SeqInfo& q) const { return (q.c * grp + kItem - 1) / kItem; }
   __device__ int first_of(const SeqInfo& q, int tile) const {
-    return window > 0 && !track ? max(0, q.r - q.c + tile * kQ / grp - window + 1) / kKeys : 0;
+    return window > 0 && !track ? max(0, q.r - q.c + tile * kItem / grp - window + 1) / kKeys : 0;
   }
   __device__ int end_of(const SeqInfo& q, int tile) const {  // key tiles [first, end) of a query tile
-    const int last = q.r - q.c + min(q.c - 1, (tile * kQ + kQ - 1) / grp);
+    const int last = q.r - q.c + min(q.c - 1, (tile * kItem + kItem - 1) / grp);
     return last < 0 ? 0 : last / kKeys + 1;
   }
   __device__ int span(const SeqInfo& q) const {  // key tiles of a query tile at most
     int n = max(1, (q.r + kKeys - 1) / kKeys);
-    if (window > 0 && !track) n = min(n, (window + kQ / grp + 1) / kKeys + 2);
+    if (window > 0 && !track) n = min(n, (window + kItem / grp + 1) / kKeys + 2);
     return n;
   }
   __device__ int splits(const SeqInfo& q) const { return (span(q) + kt - 1) / kt; }
@@ -306,19 +321,7 @@ __device__ Work make_work(const PromptArgs& a, SeqInfo* info, int* sums, bool re
   return w;
 }
 
-// ---------------------------------------------------------------- conversion: 64 rows of K and V to operands
-// What a thread (t of 128) holds of a tile before it converts it: K: 32 dims of row t / 2 per group; V: of rows
-// 4 (t % 16) .. + 3 the word t / 16 (8 dims) per group.
-template <int D>
-struct Raw {
-  static constexpr int kGroups = D / 64;
-  uint4 k[kGroups];
-  uint32_t v[kGroups][4];
-  uint32_t kp[kGroups], vp[kGroups][4];
-  int pos;
-  unsigned bad;
-};
-
+// ---------------------------------------------------------------- conversion: 64 rows of K or V to operands
 // Loads that stay where they are written: the compiler would move plain ones down to their use, a tile later.
 __device__ __forceinline__ uint32_t load_now(const uint32_t* p) {
   uint32_t r;
@@ -329,34 +332,6 @@ __device__ __forceinline__ uint4 load_now(const uint4* p) {
   uint4 r;
   asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
-}
-
-template <int D>
-__device__ __forceinline__ void load_raw(Raw<D>& w, const PromptArgs& a, const uint8_t* b0, const uint8_t* b1, int t) {
-  constexpr int kGroups = D / 64;
-  w.bad = (b0 == nullptr ? 1u : 0u) | (b1 == nullptr ? 2u : 0u);
-  const uint8_t* kb = t < 64 ? b0 : b1;         // K row t / 2
-  const uint8_t* vb = (t & 15) < 8 ? b0 : b1;   // V rows 4 (t % 16) ..
-  const int kr = (t >> 1) & 31, vr = 4 * (t & 7), vw = t >> 4;
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    w.k[g] = make_uint4(0u, 0u, 0u, 0u);
-    w.kp[g] = 0u;
-    if (kb != nullptr) {
-      w.k[g] = load_now(reinterpret_cast<const uint4*>(kb + kr * (D / 2) + g * 32 + (t & 1) * 16));
-      w.kp[g] = load_now(reinterpret_cast<const uint32_t*>(kb + code_bytes(D) + (kr * kGroups + g) * 4));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w.v[g][i] = w.vp[g][i] = 0u;
-      if (vb != nullptr) {
-        w.v[g][i] = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + (vr + i) * (D / 2) + g * 32 + vw * 4));
-        w.vp[g][i] = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + code_bytes(D) + ((vr + i) * kGroups + g) * 4));
-      }
-    }
-  }
-  w.pos = 0;
-  if (a.g.track && (t & 1) == 0 && kb != nullptr) w.pos = (int)load_now(reinterpret_cast<const uint32_t*>(kb + pos_at(D) + 4 * kr));
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
@@ -382,32 +357,69 @@ __device__ __forceinline__ uint32_t within(uint32_t pair) {
   return (pair & 0xffff0000u) | __half_as_ushort(__float2half_rd((65504.f - p.y) / 15.f));
 }
 
-// K of a tile to its stage, and what the softmax has to know: positions, bad pages, V's NaN rows, fp32: the pairs.
-template <int D, bool FP32>
-__device__ __forceinline__ void convert_k(const Raw<D>& w, const PromptArgs& a, unsigned char* kst, unsigned char* smem, int slot, int row0,
-                                          int rows, int t, TileNote* note, int* e_run) {
-  using L = Layout<D, FP32>;
-  constexpr int kGroups = D / 64;
-  const int key = t >> 1, half = t & 1, vk = 4 * (t & 15), vw = t >> 4;
-  const bool kon = row0 + key < rows;
-  if (t < 32) {  // the lanes that own V's rows here (vw 0) are in this warp
-    unsigned long long nan[2] = {0ull, 0ull};
-    if (vw == 0)
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row0 + vk + i < rows && (w.vp[g][i] & 0x7fffu) > 0x7c00u) nan[g] |= 1ull << (vk + i);
+// What a thread (t of 128) of the K warps holds of a tile before it converts it: 32 dims of row t / 2 per group, and
+// for the notes V's pair of row t % 64, group t / 64.
+template <int D>
+struct RawK {
+  static constexpr int kGroups = D / 64;
+  uint4 k[kGroups];
+  uint32_t kp[kGroups], vp;
+  int pos;
+  unsigned bad;
+  __device__ __forceinline__ void load(const PromptArgs& a, const uint8_t* b0, const uint8_t* b1, int t) {
+    bad = (b0 == nullptr ? 1u : 0u) | (b1 == nullptr ? 2u : 0u);
+    const uint8_t* kb = t < 64 ? b0 : b1;
+    const int kr = (t >> 1) & 31;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const unsigned lo = __reduce_or_sync(0xffffffffu, (unsigned)nan[g]), hi = __reduce_or_sync(0xffffffffu, (unsigned)(nan[g] >> 32));
-      if (t == 0) note->nan[g] = (unsigned long long)hi << 32 | lo;
+      k[g] = make_uint4(0u, 0u, 0u, 0u);
+      kp[g] = 0u;
+      if (kb != nullptr) {
+        k[g] = load_now(reinterpret_cast<const uint4*>(kb + kr * (D / 2) + g * 32 + (t & 1) * 16));
+        kp[g] = load_now(reinterpret_cast<const uint32_t*>(kb + code_bytes(D) + (kr * kGroups + g) * 4));
+      }
     }
-    if (t == 0) {
-      if (kGroups == 1) note->nan[1] = 0ull;
-      note->bad = w.bad;
-    }
+    pos = 0;
+    if (a.g.track && (t & 1) == 0 && kb != nullptr) pos = (int)load_now(reinterpret_cast<const uint32_t*>(kb + pos_at(D) + 4 * kr));
+    const uint8_t* vb = (t & 32) ? b1 : b0;
+    vp = 0u;
+    if (vb != nullptr && (t >> 6) < kGroups)
+      vp = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + code_bytes(D) + ((t & 31) * kGroups + (t >> 6)) * 4));
   }
+};
+// ... and of the V warps: of rows 4 (t % 16) .. + 3 the word t / 16 (8 dims) per group.
+template <int D>
+struct RawV {
+  static constexpr int kGroups = D / 64;
+  uint32_t v[kGroups][4], vp[kGroups][4];
+  __device__ __forceinline__ void load(const PromptArgs& a, const uint8_t* b0, const uint8_t* b1, int t) {
+    const uint8_t* vb = (t & 15) < 8 ? b0 : b1;
+    const int vr = 4 * (t & 7), vw = t >> 4;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[g][i] = vp[g][i] = 0u;
+        if (vb != nullptr) {
+          v[g][i] = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + (vr + i) * (D / 2) + g * 32 + vw * 4));
+          vp[g][i] = load_now(reinterpret_cast<const uint32_t*>(vb + half_bytes(D) + code_bytes(D) + ((vr + i) * kGroups + g) * 4));
+        }
+      }
+  }
+};
+
+// K of a tile to its stage, and what the softmax has to know: positions, bad pages, V's NaN rows, fp32: the pairs.
+template <int D, bool FP32>
+__device__ __forceinline__ void convert_k(const RawK<D>& w, const PromptArgs& a, unsigned char* kst, unsigned char* smem, int slot, int row0,
+                                          int rows, int t, TileNote* note) {
+  using L = Layout<D, FP32>;
+  constexpr int kGroups = D / 64;
+  const int key = t >> 1, half = t & 1;
+  const bool kon = row0 + key < rows, von = row0 + (t & 63) < rows;
+  const unsigned nan = __ballot_sync(0xffffffffu, von && (w.vp & 0x7fffu) > 0x7c00u);
+  const uint32_t vp = von && (w.vp & 0x7fffu) <= 0x7c00u ? w.vp : 0u;
+  if ((t & 31) == 0) note->nan[t >> 6][(t >> 5) & 1] = nan;
+  if (t == 0) note->bad = w.bad;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     // four chunks of 8 dims, in the order 0 4 1 5 2 6 3 7 (q is stored in the same order)
@@ -425,40 +437,27 @@ __device__ __forceinline__ void convert_k(const Raw<D>& w, const PromptArgs& a, 
     }
   }
   if (FP32) {
-    // the rows' pairs, lo moved to the codes' middle; V's scales in units of 2^(e - 6), e being the exponent of the
-    // largest so far, so that scale times a weight of at most 2^8 stays below 2^15
+    // the rows' pairs, lo moved to the codes' middle, and V's largest scale
     float* pairs = reinterpret_cast<float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
     if (half == 0) {
       const float2 p = unpack_half(kon ? w.kp[0] : 0u);
       pairs[key] = p.x;
       pairs[kKeys + key] = fmaf(8.f, p.x, p.y);
     }
-    int e = -15;
-    uint32_t vp[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // every warp has all 64 rows: one exponent for all, without a barrier
-      vp[i] = row0 + vk + i < rows && (w.vp[0][i] & 0x7fffu) <= 0x7c00u ? w.vp[0][i] : 0u;
-      e = max(e, min((int)((vp[i] >> 10) & 31u) - 15, 15));
+    if (t < 64) {
+      const float2 p = unpack_half(vp);
+      pairs[2 * kKeys + t] = p.x;
+      pairs[3 * kKeys + t] = fmaf(8.f, p.x, p.y);
+      const unsigned e = __reduce_max_sync(0xffffffffu, (vp >> 10) & 31u);
+      if ((t & 31) == 0) note->e[t >> 5] = min((int)e - 15, 15);
     }
-    e = (int)__reduce_max_sync(0xffffffffu, (unsigned)(e + 32)) - 32;
-    *e_run = max(*e_run, e);
-    if (vw == 0) {
-      const float unit = pow2i(6 - *e_run);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack_half(vp[i]);
-        pairs[2 * kKeys + vk + i] = p.x * unit;
-        pairs[3 * kKeys + vk + i] = fmaf(8.f, p.x, p.y);
-      }
-    }
-    if (t == 0) note->e = *e_run;
   }
   if (a.g.track && half == 0) reinterpret_cast<int*>(smem + L::kPosAt)[slot * kKeys + key] = w.pos;
 }
 
 // V of a tile to its stage, transposed: of rows vk .. vk + 3, 8 bytes of each of 8 dims' rows.
 template <int D, bool FP32>
-__device__ __forceinline__ void convert_v(const Raw<D>& w, unsigned char* vst, int row0, int rows, int t) {
+__device__ __forceinline__ void convert_v(const RawV<D>& w, unsigned char* vst, int row0, int rows, int t) {
   constexpr int kGroups = D / 64;
   const int vk = 4 * (t & 15), vw = t >> 4;
 #pragma unroll
@@ -495,18 +494,18 @@ __device__ __forceinline__ void convert_v(const Raw<D>& w, unsigned char* vst, i
 
 // ---------------------------------------------------------------- the kernel
 template <int D, bool FP32, bool FEAT>
-__global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
   using L = Layout<D, FP32>;
   constexpr int kGroups = D / 64;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], pv_done[2], p_full, q_full, drain;
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], pv_done[2][2], p_full[2], q_full, drain;  // [query tile][stage]
   __shared__ uint32_t tmem_slot;
   __shared__ unsigned failed;
   __shared__ TileNote notes[kNotes];
   __shared__ int sums[kThreads / 32];
   unsigned char* smem = raw_smem + ((1024u - (smem_of(raw_smem) & 1023u)) & 1023u);
   SeqInfo* info = reinterpret_cast<SeqInfo*>(smem + L::kInfoAt);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -514,16 +513,18 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 128);
       mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 2);
-      mbar_init(&pv_done[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[h][i], 2);
+        mbar_init(&pv_done[h][i], 1);
+      }
+      mbar_init(&p_full[i], 128);
     }
+    mbar_init(&q_full, 256);
     mbar_init(&drain, 1);
-    mbar_init(&p_full, 128);
-    mbar_init(&q_full, 128);
     failed = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 7) {
+  if (warp == 15) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&tmem_slot)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -533,52 +534,71 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
   fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = tmem_slot;
-  const uint32_t t_out = tmem + 2 * kKeys, t_sum = t_out + 64;  // fp32: sums behind the output
   volatile unsigned* abort = &failed;
   unsigned tile_no = 0;  // key tiles so far: every role counts them alike
 
-  if (warp >= 4) {
-    // ------------------------------------------------------------ conversion and matrix instructions
+  if (warp >= 8) {
+    // ------------------------------------------------------------ conversion (warps 8 .. 11: K, 12 .. 15: V) and matrix instructions
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");  // of 128 at launch; the softmax takes them
-    const int t = threadIdx.x - 128;
+    const bool for_k = warp < 12;
+    const int t = threadIdx.x & 127;
     bool ok = true;
     // descriptors of the operands' first tiles; 16 bytes on are 1 more
-    const uint64_t q_desc = tile_desc(smem_of(smem + L::kQAt));
-    const uint64_t k_desc = tile_desc(smem_of(smem + L::kKAt)), v_desc = tile_desc(smem_of(smem + L::kVAt));
+    const uint64_t q_desc = tile_desc(smem_of(smem + L::kQAt)), k_desc = tile_desc(smem_of(smem + L::kKAt)), v_desc = tile_desc(smem_of(smem + L::kVAt));
     unsigned items = 0;
-    // (lane 0 of warp 4) S = Q K^T of key tile number `no`, the item's j-th
+    // (warp 8) S = Q K^T of key tile number `no`, the item's j-th, for both query tiles; ST: the tile's stage
+    auto score_at = [&](auto ST) {
+      constexpr int st = decltype(ST)::value;
+      if (elected()) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma(tmem + h * 256 + st * kKeys, q_desc + h * (L::kQTile / 16) + (hf * kGroups + g) * (kQ * 8) + ks * 2,
+                     k_desc + st * (L::kTile / 16) + g * (kKeys * 8) + ks * 2, idesc(kKeys), hf + g + ks > 0 ? 1u : 0u);
+          umma_commit(&s_full[h][st]);
+          mbar_arrive(&s_full[h][st]);  // and orders the conversion's notes before the softmax
+        }
+        umma_commit(&k_empty[st]);
+      }
+      __syncwarp();
+    };
     auto score = [&](unsigned no, int j) {
-      if (j == 0 && !mbar_wait(&q_full, items & 1, abort)) return false;
-      if (!mbar_wait(&k_full[no & 1], (no >> 1) & 1, abort)) return false;
+      if (j == 0 && !warp_wait(&q_full, items & 1, abort)) return false;
+      if (!warp_wait(&k_full[no & 1], (no >> 1) & 1, abort)) return false;
       fence_after();
-      const uint64_t kd = k_desc + (no & 1) * (L::kTile / 16);
-      const uint32_t d = tmem + (no & 1) * kKeys;
-#pragma unroll
-      for (int hf = 0; hf < L::kHalves; ++hf)
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma(d, q_desc + (hf * kGroups + g) * (kQ * 8) + ks * 2, kd + g * (kKeys * 8) + ks * 2, idesc(kKeys), hf + g + ks > 0 ? 1u : 0u);
-      umma_commit(&k_empty[no & 1]);
-      umma_commit(&s_full[no & 1]);
-      mbar_arrive(&s_full[no & 1]);  // and orders the conversion's notes before the softmax
+      if (no & 1) score_at(Const<1>{}); else score_at(Const<0>{});
       return true;
     };
-    // (the same lane) O += P V
+    // (the same warp) O += P V
+    auto product_at = [&](auto ST, int h, bool fresh) {
+      constexpr int st = decltype(ST)::value;
+      if (elected()) {
+        const uint32_t base = tmem + h * 256;
+#pragma unroll
+        for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)  // 32 keys' weights, hi and lo, lie in the 32 columns of their scores
+            umma_tmem(base + 2 * kKeys, base + st * kKeys + (ks >> 1) * 32 + hf * 16 + (ks & 1) * 8, v_desc + st * (L::kTile / 16) + ks * 2,
+                      idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
+        umma_commit(&pv_done[h][st]);
+        if (h == 1) umma_commit(&v_empty[st]);
+      }
+      __syncwarp();
+    };
     auto product = [&](unsigned no, int j) {
-      const int st = no & 1;
-      if (!mbar_wait(&v_full[st], (no >> 1) & 1, abort) || !mbar_wait(&p_full, no & 1, abort)) return false;
-      fence_after();
-      const uint64_t vd = v_desc + st * (L::kTile / 16);
+      if (!warp_wait(&v_full[no & 1], (no >> 1) & 1, abort)) return false;
       const bool fresh = FP32 ? j % kFlush == 0 : j == 0;
 #pragma unroll
-      for (int hf = 0; hf < L::kHalves; ++hf)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)  // 32 keys' weights, hi and lo, lie in the 32 columns of their scores
-          umma_tmem(t_out, tmem + st * kKeys + (ks >> 1) * 32 + hf * 16 + (ks & 1) * 8, vd + ks * 2, idesc(D), hf + ks > 0 || !fresh ? 1u : 0u);
-      umma_commit(&v_empty[st]);
-      umma_commit(&pv_done[st]);
+      for (int h = 0; h < 2; ++h) {
+        if (!warp_wait(&p_full[h], no & 1, abort)) return false;
+        fence_after();
+        if (no & 1) product_at(Const<1>{}, h, fresh); else product_at(Const<0>{}, h, fresh);
+      }
       return true;
     };
     for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
@@ -597,55 +617,64 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
         return a.g.pool + (size_t)pg * a.g.page_stride + (size_t)(a.layer * a.g.nkv + it.h) * a.g.head_stride +
                (unsigned)(((row & ((1 << a.g.page_shift) - 1)) / kRows) * a.g.block_bytes);
       };
-      Raw<D> cur;
-      {
-        const int r = it.k0 * kKeys;
-        load_raw<D>(cur, a, block(r, page(r)), block(r + kRows, page(r + kRows)), t);
-      }
-      int p0 = page((it.k0 + 1) * kKeys), p1 = page((it.k0 + 1) * kKeys + kRows);
-      int e_run = -15;
-      for (int k = it.k0; k < it.k1; ++k, ++tile_no) {
-        Raw<D> nxt;
-        if (k + 1 < it.k1) {
-          const int r = (k + 1) * kKeys;
-          load_raw<D>(nxt, a, block(r, p0), block(r + kRows, p1), t);
-          p0 = page(r + kKeys);
-          p1 = page(r + kKeys + kRows);
+      auto run = [&](auto& cur, auto& nxt, auto&& step) {
+        {
+          const int r = it.k0 * kKeys;
+          cur.load(a, block(r, page(r)), block(r + kRows, page(r + kRows)), t);
         }
-        const int st = tile_no & 1, slot = tile_no % kNotes;
-        cur.bad &= k * kKeys + kRows < sq.r ? 3u : 1u;  // a block behind the cache's end has no page: not an error
-        if (tile_no >= 2 && !(ok = warp_wait(&k_empty[st], ((tile_no >> 1) - 1) & 1, abort))) break;
-        convert_k<D, FP32>(cur, a, smem + L::kKAt + st * L::kTile, smem, slot, k * kKeys, sq.r, t, &notes[slot], &e_run);
-        fence_async();
-        mbar_arrive(&k_full[st]);
-        if (tile_no >= 2 && !(ok = warp_wait(&v_empty[st], ((tile_no >> 1) - 1) & 1, abort))) break;
-        convert_v<D, FP32>(cur, smem + L::kVAt + st * L::kTile, k * kKeys, sq.r, t);
-        fence_async();
-        mbar_arrive(&v_full[st]);
-        if (t == 0) ok = score(tile_no, k - it.k0) && (k == it.k0 || product(tile_no - 1, k - it.k0 - 1));
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        cur = nxt;
+        int p0 = page((it.k0 + 1) * kKeys), p1 = page((it.k0 + 1) * kKeys + kRows);
+        for (int k = it.k0; ok && k < it.k1; ++k, ++tile_no) {
+          if (k + 1 < it.k1) {
+            const int r = (k + 1) * kKeys;
+            nxt.load(a, block(r, p0), block(r + kRows, p1), t);
+            p0 = page(r + kKeys);
+            p1 = page(r + kKeys + kRows);
+          }
+          ok = step(cur, k);
+          cur = nxt;
+        }
+      };
+      if (for_k) {
+        RawK<D> cur, nxt;
+        run(cur, nxt, [&](RawK<D>& w, int k) {
+          const int st = tile_no & 1, slot = tile_no % kNotes;
+          w.bad &= k * kKeys + kRows < sq.r ? 3u : 1u;  // a block behind the cache's end has no page: not an error
+          if (tile_no >= 2 && !warp_wait(&k_empty[st], ((tile_no >> 1) - 1) & 1, abort)) return false;
+          convert_k<D, FP32>(w, a, smem + L::kKAt + st * L::kTile, smem, slot, k * kKeys, sq.r, t, &notes[slot]);
+          fence_async();
+          mbar_arrive(&k_full[st]);
+          return warp != 8 || (score(tile_no, k - it.k0) && (k == it.k0 || product(tile_no - 1, k - it.k0 - 1)));
+        });
+        if (ok && warp == 8) ok = product(tile_no - 1, it.k1 - it.k0 - 1);
+      } else {
+        RawV<D> cur, nxt;
+        run(cur, nxt, [&](RawV<D>& w, int k) {
+          const int st = tile_no & 1;
+          if (tile_no >= 2 && !warp_wait(&v_empty[st], ((tile_no >> 1) - 1) & 1, abort)) return false;
+          convert_v<D, FP32>(w, smem + L::kVAt + st * L::kTile, k * kKeys, sq.r, t);
+          fence_async();
+          mbar_arrive(&v_full[st]);
+          return true;
+        });
       }
-      if (ok && t == 0) ok = product(tile_no - 1, it.k1 - it.k0 - 1);
-      ok = __all_sync(0xffffffffu, ok);
       ++items;
     }
   } else {
     // ------------------------------------------------------------ softmax: one query row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    const int row = threadIdx.x;
-    const uint32_t lane_at = (uint32_t)(warp * 32) << 16;
+    const int h = warp >> 2, row = threadIdx.x & 127;  // query tile, row
+    const uint32_t mine = tmem + h * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_out = mine + 2 * kKeys, t_sum = t_out + 64;  // this lane's columns
     bool ok = true;
     for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
       const Item it = item_at(work, i);
       const SeqInfo sq = info[it.s];
       if (it.k0 >= it.k1 && (it.parts > 0 || it.split > 0)) continue;
-      const int qrow = it.tile * kQ + row, tok = qrow / a.grp, head = it.h * a.grp + qrow - tok * a.grp;
+      const int qrow0 = it.tile * kItem + h * kQ, qrow = qrow0 + row, tok = qrow / a.grp, head = it.h * a.grp + qrow - tok * a.grp;
       const bool on = tok < sq.c;
       const int limit = on ? sq.r - sq.c + tok : -1;
-      const int first_limit = sq.r - sq.c + it.tile * kQ / a.grp;
-      const int last_limit = sq.r - sq.c + min(sq.c - 1, (it.tile * kQ + kQ - 1) / a.grp);
-      const bool whole_tile = (it.tile + 1) * kQ <= sq.c * a.grp;
+      const int first_limit = sq.r - sq.c + qrow0 / a.grp;
+      const int last_limit = sq.r - sq.c + min(sq.c - 1, (qrow0 + kQ - 1) / a.grp);
+      const bool whole_tile = qrow0 + kQ <= sq.c * a.grp;
       const int qpos = FEAT && on ? (a.b.positions != nullptr ? a.b.positions[it.s] : sq.r - sq.c) + tok : 0;
       const float slope = FEAT && on && a.a.slopes != nullptr ? a.a.slopes[head] * kLog2e : 0.f;
       // the row of q to the operand, its largest element scaled to [2^13, 2^14)
@@ -686,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
             const float2 u = unpack_half(hi[e]);
             lo[e] = pack_half(x0 - u.x, x1 - u.y);
           }
-          unsigned char* q = smem + L::kQAt + (c >> 3) * kQ * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          unsigned char* q = smem + L::kQAt + h * L::kQTile + (c >> 3) * kQ * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
           *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if (FP32) *reinterpret_cast<uint4*>(q + kGroups * kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
@@ -701,11 +730,11 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       unsigned nan_groups = 0u;
       for (int k = it.k0; k < it.k1; ++k, ++tile_no) {
         const int st = tile_no & 1, slot = tile_no % kNotes, j = k - it.k0;
-        if (!(ok = warp_wait(&s_full[st], (tile_no >> 1) & 1, abort))) break;
+        if (!(ok = warp_wait(&s_full[h][st], (tile_no >> 1) & 1, abort))) break;
         fence_after();
         f2 x[kKeys / 2];
-        tmem_ld32(tmem + lane_at + st * kKeys, x);
-        tmem_ld32(tmem + lane_at + st * kKeys + 32, x + 16);
+        tmem_ld32(mine + st * kKeys, x);
+        tmem_ld32(mine + st * kKeys + 32, x + 16);
         const float* pairs = reinterpret_cast<const float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
         const TileNote note = notes[slot];
         tmem_wait_ld();
@@ -756,12 +785,12 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
             x[c] = pair_of(at > lim ? -INFINITY : v.x, at + 1 > lim ? -INFINITY : v.y);
           }
         }
-        if ((note.nan[0] | note.nan[1]) != 0ull) {
+        if ((note.nan[0][0] | note.nan[0][1] | note.nan[1][0] | note.nan[1][1]) != 0u) {
           // rows of V that are NaN: the output of those who see them is NaN
 #pragma unroll
           for (int c = 0; c < kKeys / 2; ++c) {
             const float2 v = halves(x[c]);
-            const unsigned b0 = (unsigned)(note.nan[0] >> (2 * c)), b1 = (unsigned)(note.nan[1] >> (2 * c));
+            const unsigned b0 = note.nan[0][c >> 4] >> (2 * (c & 15)), b1 = note.nan[1][c >> 4] >> (2 * (c & 15));
             if (!(v.x == -INFINITY)) nan_groups |= (b0 & 1u) | (b1 & 1u) << 1;
             if (!(v.y == -INFINITY)) nan_groups |= (b0 >> 1 & 1u) | (b1 & 2u);
           }
@@ -775,46 +804,48 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
         }
         top = fmaxf(top, top1);
         top = FEAT || top == -INFINITY ? top : top * mul;
-        const bool renew = __any_sync(0xffffffffu, top > m + kSlack) || (FP32 && note.e != e_cur), flush = FP32 && j > 0 && j % kFlush == 0;
+        const int e_new = FP32 ? max(e_cur, max(note.e[0], note.e[1])) : 0;
+        const bool renew = __any_sync(0xffffffffu, top > m + kSlack) || (FP32 && e_new != e_cur), flush = FP32 && j > 0 && j % kFlush == 0;
         float rescale = 1.f;
         if (renew) {
           const float nm = fmaxf(m, top);
-          rescale = nm == -INFINITY ? 1.f : ex2(m - nm);
+          // (fp32: the weights' unit goes with V's largest scale; see below)
+          rescale = nm == -INFINITY ? 1.f : ex2(m - nm + (FP32 ? (float)(e_cur - e_new) : 0.f));
           m = nm;
           l = mul2(l, pair_of(rescale, rescale));
           z = mul2(z, pair_of(rescale, rescale));
-          if (FP32) rescale *= pow2i(e_cur - note.e);
-          e_cur = note.e;
+          e_cur = e_new;
         }
         if (j > 0 && (renew || flush)) {
           // the output, once the product before has left it
-          if (!(ok = warp_wait(&pv_done[st ^ 1], ((tile_no - 1) >> 1) & 1, abort))) break;
+          if (!(ok = warp_wait(&pv_done[h][st ^ 1], ((tile_no - 1) >> 1) & 1, abort))) break;
           fence_after();
           if (flush) {  // moved to the sums
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
               float o[16], s[16];
-              tmem_ld16(t_out + lane_at + c, o);
-              if (j > kFlush) tmem_ld16(t_sum + lane_at + c, s);
+              tmem_ld16(t_out + c, o);
+              if (j > kFlush) tmem_ld16(t_sum + c, s);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = (j > kFlush ? o[e] + s[e] : o[e]) * rescale;
-              tmem_st16(t_sum + lane_at + c, o);
+              tmem_st16(t_sum + c, o);
             }
           } else {
 #pragma unroll 1
             for (int c = 0; c < (FP32 && j > kFlush ? 128 : D); c += 16) {
               float o[16];
-              tmem_ld16(t_out + lane_at + c, o);
+              tmem_ld16(t_out + c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] *= rescale;
-              tmem_st16(t_out + lane_at + c, o);
+              tmem_st16(t_out + c, o);
             }
           }
         }
         // the weights, 32 keys at a time over their own scores: 16 columns of hi, fp32: 16 of lo
-        const float base = m == -INFINITY ? 0.f : m;
+        // (fp32: times 2^(6 - e), e the exponent of V's largest scale: a weight of at most 2^8 times a scale is below 2^15)
+        const float base = (m == -INFINITY ? 0.f : m) + (FP32 ? (float)(e_cur - 6) : 0.f);
         const f2 by = FEAT ? pair_of(1.f, 1.f) : pair_of(mul, mul), less = pair_of(-base, -base), minus = pair_of(-1.f, -1.f);
 #pragma unroll
         for (int c0 = 0; c0 < kKeys / 2; c0 += 16) {
@@ -836,38 +867,38 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
               lo[c] = pack_half(v.x, v.y);
             }
           }
-          tmem_st16(tmem + lane_at + st * kKeys + 2 * c0, hi);
-          if (FP32) tmem_st16(tmem + lane_at + st * kKeys + 2 * c0 + 16, lo);
+          tmem_st16(mine + st * kKeys + 2 * c0, hi);
+          if (FP32) tmem_st16(mine + st * kKeys + 2 * c0 + 16, lo);
         }
         tmem_wait_st();
         fence_before();
-        mbar_arrive(&p_full);
+        mbar_arrive(&p_full[h]);
       }
       if (!ok) break;
       const int n = it.k1 - it.k0;
       if (n > 0) {
-        if (!(ok = warp_wait(&pv_done[(tile_no - 1) & 1], ((tile_no - 1) >> 1) & 1, abort))) break;
+        if (!(ok = warp_wait(&pv_done[h][(tile_no - 1) & 1], ((tile_no - 1) >> 1) & 1, abort))) break;
         fence_after();
       }
       // the output, or the run's partial
       const bool last = it.parts <= 1;
       const float sum_l = halves(l).x + halves(l).y, sum_z = halves(z).x + halves(z).y;
       const float inv = last ? (sum_l > 0.f || sum_l != sum_l ? 1.f / sum_l : 0.f) : 1.f;
-      const float unit = FP32 ? pow2i(e_cur - 6) : 1.f;
-      float* part = last ? nullptr : a.part + ((size_t)i * kQ + row) * (D + 4);
+      const float m_ref = m + (FP32 ? (float)(e_cur - 6) : 0.f);  // what l and the output are relative to
+      float* part = last ? nullptr : a.part + ((size_t)i * kItem + h * kQ + row) * (D + 4);
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         float o[16], s[16];
         __syncwarp();
         if (n > 0) {
-          tmem_ld16(t_out + lane_at + c, o);
-          if (FP32 && n > kFlush) tmem_ld16(t_sum + lane_at + c, s);
+          tmem_ld16(t_out + c, o);
+          if (FP32 && n > kFlush) tmem_ld16(t_sum + c, s);
           tmem_wait_ld();
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           if (FP32 && n > kFlush) o[e] += s[e];
-          o[e] = n > 0 ? (FP32 ? fmaf(o[e], unit, sum_z) : o[e]) * inv : 0.f;
+          o[e] = n > 0 ? (FP32 ? o[e] + sum_z : o[e]) * inv : 0.f;
           if (nan_groups >> (c >> 6) & 1u) o[e] = NAN;
         }
         if (on) {
@@ -889,10 +920,10 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
       }
       if (on) {
         if (!last) {
-          part[D] = m;
+          part[D] = m_ref;
           part[D + 1] = sum_l;
         } else if (a.lse != nullptr) {
-          a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = sum_l > 0.f ? m + log2f(sum_l) : INFINITY;
+          a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = sum_l > 0.f ? m_ref + log2f(sum_l) : INFINITY;
         }
       }
       __syncwarp();
@@ -902,15 +933,16 @@ __global__ void __launch_bounds__(kThreads, 2) prompt_kernel(const __grid_consta
   __syncwarp();
   __syncthreads();
   if (failed != 0u && threadIdx.x == 0) flag(a.b.status, MBK_KV4_TIMEOUT);
-  if (failed != 0u && warp == 4 && lane == 0) {
+  if (failed != 0u && warp == 8) {
     // matrix instructions in flight end before their tensor memory is freed
-    umma_commit(&drain);
+    if (elected()) umma_commit(&drain);
+    __syncwarp();
     for (int i = 0; i < 20000000 && !mbar_test(&drain, 0); ++i) {
     }
   }
   fence_before();
   __syncthreads();
-  if (warp == 7) {
+  if (warp == 15) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
@@ -928,8 +960,8 @@ __global__ void __launch_bounds__(512) prompt_combine_kernel(const __grid_consta
     if (it.split != 0 || it.parts <= 1) continue;
     const SeqInfo sq = w.seq[it.s];
     // the splits of a (tile, head) are nkv items apart
-    join<D>(a, sq, it.h, it.tile * kQ, min(kQ, sq.c * a.grp - it.tile * kQ), it.parts, nullptr,
-            [&](int k) { return a.part + (size_t)(i + k * w.nkv) * kQ * (D + 4); });
+    join<D>(a, sq, it.h, it.tile * kItem, min(kItem, sq.c * a.grp - it.tile * kItem), it.parts, nullptr,
+            [&](int k) { return a.part + (size_t)(i + k * w.nkv) * kItem * (D + 4); });
   }
 }
 
@@ -937,8 +969,8 @@ template <int D, bool FP32, bool FEAT>
 cudaError_t run(const PromptArgs& a, cudaStream_t st) {
   static std::atomic<bool> once[64];
   const size_t smem = 1024 + Layout<D, FP32>::kInfoAt + (size_t)a.b.n_seq * sizeof(SeqInfo);
-  if (cudaError_t e = allow_smem((const void*)prompt_kernel<D, FP32, FEAT>, once, 112 * 1024)) return e;
-  const long long tiles = ((long long)a.b.max_count * a.grp + kQ - 1) / kQ;
+  if (cudaError_t e = allow_smem((const void*)prompt_kernel<D, FP32, FEAT>, once, 224 * 1024)) return e;
+  const long long tiles = ((long long)a.b.max_count * a.grp + kItem - 1) / kItem;
   const long long items = a.b.n_seq * (long long)a.g.nkv * tiles * ((a.b.max_rows + kKeys - 1) / kKeys / kMinRun + 1);
   const int grid = (int)std::max<long long>(1, std::min<long long>(a.slots, items));
   if (cudaError_t e = launch(prompt_kernel<D, FP32, FEAT>, dim3(grid), kThreads, smem, st, false, a)) return e;
@@ -949,9 +981,9 @@ cudaError_t run(const PromptArgs& a, cudaStream_t st) {
 
 size_t kv4_prompt_partials(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
   // split tiles are fewer than 2 x slots, and have at most kMaxRounds x slots runs and one more each
-  const long long tiles = ((long long)b.max_count * (g.nq / g.nkv) + kQ - 1) / kQ * g.nkv * b.n_seq;
+  const long long tiles = ((long long)b.max_count * (g.nq / g.nkv) + kItem - 1) / kItem * g.nkv * b.n_seq;
   const long long runs = (b.max_rows + kKeys - 1) / kKeys / kMinRun + 1;
-  return (size_t)std::min<long long>((kMaxRounds + 2ll) * 2 * num_sms, tiles * runs) * kQ * (g.d + 4) * 4;
+  return (size_t)std::min<long long>((kMaxRounds + 2ll) * num_sms, tiles * runs) * kItem * (g.d + 4) * 4;
 }
 
 cudaError_t kv4_prompt(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4Attn& at, int least, float* part, float* lse, int num_sms,
@@ -963,7 +995,7 @@ cudaError_t kv4_prompt(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4
   a.layer = layer;
   a.grp = g.nq / g.nkv;
   a.least = least;
-  a.slots = 2 * num_sms;
+  a.slots = num_sms;
   a.scale2 = at.scale * kLog2e;
   a.cap_in = at.cap > 0.f ? 2.f / at.cap : 0.f;
   a.cap_out = at.cap * kLog2e;
