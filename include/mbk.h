@@ -339,7 +339,7 @@ typedef struct {
   int32_t max_rows;         /* no sequence has more rows; at most max_pages * page_size */
   const int32_t *offsets;   /* [n_seq + 1] */
   const int32_t *rows;      /* [n_seq] */
-  const int32_t *positions; /* [n_seq] position of the first new token, or NULL: the index of its row */
+  const int32_t *positions; /* [n_seq] position of the first new token, or NULL: the index of its row (NULL unless track = 1) */
   const int32_t *tables;    /* [n_seq][max_pages] page of rows q * page_size .. */
   int32_t *status;          /* one word, or NULL */
 } mbk_kv4_batch;

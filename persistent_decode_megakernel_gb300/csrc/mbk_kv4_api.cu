@@ -45,7 +45,8 @@ int sms_of(int device) {
 
 bool batch_ok(const mbk_kv4_config& c, const mbk_kv4_batch* b) {
   if (!b || b->n_seq < 1 || b->n_seq > MBK_KV4_MAX_SEQS || b->n_tokens < 1 || b->max_count < 1 || b->max_count > b->n_tokens ||
-      b->max_rows < 0 || (int64_t)b->max_rows > (int64_t)c.max_pages * c.page_size || !b->offsets || !b->rows || !b->tables)
+      b->max_rows < 0 || (int64_t)b->max_rows > (int64_t)c.max_pages * c.page_size || !b->offsets || !b->rows || !b->tables ||
+      (b->positions && !c.track))
     return false;
   return aligned4(b->offsets) && aligned4(b->rows) && aligned4(b->positions) && aligned4(b->tables) && aligned4(b->status);
 }

@@ -538,10 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   unsigned tile_no = 0;  // key tiles so far: every role counts them alike
 
   if (warp >= 8) {
-    // ------------------------------------------------------------ conversion (warps 8 .. 11: K, 12 .. 15: V) and matrix instructions
+    // ------------------------------------------------------------ conversion (warps 8, 9, 12, 13: K, the others: V) and matrix instructions
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");  // of 128 at launch; the softmax takes them
-    const bool for_k = warp < 12;
-    const int t = threadIdx.x & 127;
+    // two warps of one kind on a scheduler (warp % 4), not one of each: it then has less code to fetch
+    const bool for_k = (warp & 2) == 0;
+    const int t = (warp >= 12 ? 64 : 0) + (warp & 1) * 32 + (threadIdx.x & 31);
     bool ok = true;
     // descriptors of the operands' first tiles; 16 bytes on are 1 more
     const uint64_t q_desc = tile_desc(smem_of(smem + L::kQAt)), k_desc = tile_desc(smem_of(smem + L::kKAt)), v_desc = tile_desc(smem_of(smem + L::kVAt));
@@ -671,28 +672,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (it.k0 >= it.k1 && (it.parts > 0 || it.split > 0)) continue;
       const int qrow0 = it.tile * kItem + h * kQ, qrow = qrow0 + row, tok = qrow / a.grp, head = it.h * a.grp + qrow - tok * a.grp;
       const bool on = tok < sq.c;
+      auto qpos_of = [&](int token) { return (FEAT && a.b.positions != nullptr ? a.b.positions[it.s] : sq.r - sq.c) + token; };
       const int limit = on ? sq.r - sq.c + tok : -1;
       const int first_limit = sq.r - sq.c + qrow0 / a.grp;
-      const int last_limit = sq.r - sq.c + min(sq.c - 1, (qrow0 + kQ - 1) / a.grp);
       const bool whole_tile = qrow0 + kQ <= sq.c * a.grp;
-      const int qpos = FEAT && on ? (a.b.positions != nullptr ? a.b.positions[it.s] : sq.r - sq.c) + tok : 0;
+      // first row inside the window of this query and of the tile's last, where positions are the rows' numbers
+      const bool by_row = FEAT && a.a.window > 0 && !a.g.track;
+      const int low = by_row ? qpos_of(tok) - a.a.window + 1 : 0, last_low = by_row ? qpos_of(min(sq.c - 1, (qrow0 + kQ - 1) / a.grp)) - a.a.window + 1 : 0;
+      const int qpos = FEAT && on ? qpos_of(tok) : 0;
       const float slope = FEAT && on && a.a.slopes != nullptr ? a.a.slopes[head] * kLog2e : 0.f;
       // the row of q to the operand, its largest element scaled to [2^13, 2^14)
       float mul, addm = 0.f;  // score = mul * (acc, or fp32: scale_r acc + z_r addm)
       {
         float mx = 0.f, sum = 0.f;
         const size_t at = (size_t)(sq.tok0 + (on ? tok : 0)) * a.a.ldq + (size_t)head * D;
-        auto load = [&](int c, float(&x)[8]) {
+        // the whole row at once: 64 registers, one wait
+        constexpr int kVec = FP32 ? D / 4 : D / 8;
+        uint4 q[kVec];
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(a.a.q) + at * (FP32 ? 4 : 2));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = 0.f;
-          if (on) {
-            if (FP32) load8<float>(reinterpret_cast<const float*>(a.a.q) + at + 8 * c, x);
-            else load8<__nv_bfloat16>(reinterpret_cast<const __nv_bfloat16*>(a.a.q) + at + 8 * c, x);
+        for (int c = 0; c < kVec; ++c) q[c] = on ? __ldg(from + c) : make_uint4(0u, 0u, 0u, 0u);
+        auto get = [&](int c, float(&x)[8]) {
+          if (FP32) {
+            const uint4 u = q[(2 * c) % kVec], v = q[(2 * c + 1) % kVec];
+            x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+            x[4] = __uint_as_float(v.x), x[5] = __uint_as_float(v.y), x[6] = __uint_as_float(v.z), x[7] = __uint_as_float(v.w);
+          } else {
+            const uint32_t w[4] = {q[c % kVec].x, q[c % kVec].y, q[c % kVec].z, q[c % kVec].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(w[e] << 16);
+              x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
           }
         };
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           float x[8];
-          load(c, x);
+          get(c, x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             mx = fmaxf(mx, fabsf(x[e]));
@@ -704,9 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const float up = a.scale2 < 0.f ? -pow2i(140 - ex) : pow2i(140 - ex);  // mul >= 0: the largest acc is the largest score
         mul = pow2i(ex - 140) * fabsf(a.scale2);
         if (FP32) addm = sum * up;
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           float x[8];
-          load(c, x);
+          get(c, x);
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // the conversion's order of dims: 0 4 1 5 2 6 3 7
@@ -715,9 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const float2 u = unpack_half(hi[e]);
             lo[e] = pack_half(x0 - u.x, x1 - u.y);
           }
-          unsigned char* q = smem + L::kQAt + h * L::kQTile + (c >> 3) * kQ * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (FP32) *reinterpret_cast<uint4*>(q + kGroups * kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          unsigned char* to = smem + L::kQAt + h * L::kQTile + (c >> 3) * kQ * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (FP32) *reinterpret_cast<uint4*>(to + kGroups * kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       if (it.k0 < it.k1) {
@@ -762,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
             for (int c = 0; c < kKeys / 2; ++c) x[c] = mul2(x[c], all);
           }
-          // distances, where there is a bias, or a window that leaves out some row of the tile for some query
-          if (a.a.slopes != nullptr || (a.a.window > 0 && (a.g.track || k * kKeys <= last_limit - a.a.window))) {
+          // distances, where there is a bias or positions are not the rows' numbers
+          if (a.a.slopes != nullptr || (a.a.window > 0 && a.g.track)) {
             const int* pos = reinterpret_cast<const int*>(smem + L::kPosAt) + slot * kKeys;
             const int win = a.a.window > 0 ? -a.a.window : -0x7fffffff - 1;
 #pragma unroll
@@ -777,12 +795,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
           }
         }
-        if ((k + 1) * kKeys - 1 > first_limit || !whole_tile || note.bad != 0u) {
+        if ((k + 1) * kKeys - 1 > first_limit || !whole_tile || note.bad != 0u || (FEAT && k * kKeys < last_low)) {
 #pragma unroll
           for (int c = 0; c < kKeys / 2; ++c) {
             const int lim = (note.bad >> (c >> 4)) & 1u ? -1 : limit, at = k * kKeys + 2 * c;
             const float2 v = halves(x[c]);
-            x[c] = pair_of(at > lim ? -INFINITY : v.x, at + 1 > lim ? -INFINITY : v.y);
+            x[c] = pair_of(at > lim || (FEAT && at < low) ? -INFINITY : v.x, at + 1 > lim || (FEAT && at + 1 < low) ? -INFINITY : v.y);
           }
         }
         if ((note.nan[0][0] | note.nan[0][1] | note.nan[1][0] | note.nan[1][1]) != 0u) {
@@ -950,18 +968,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
 // Joins the runs of query tiles whose keys were split.
 template <int D>
-__global__ void __launch_bounds__(512) prompt_combine_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_constant__ PromptArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int sums[16];
   const Work w = make_work(a, reinterpret_cast<SeqInfo*>(smem), sums, false);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int i = blockIdx.x; i < w.total; i += gridDim.x) {
+  constexpr int kPiece = 32;  // rows at a time
+  for (int x = blockIdx.x; x < w.total * (kItem / kPiece); x += gridDim.x) {
+    const int i = x / (kItem / kPiece), row0 = x % (kItem / kPiece) * kPiece;
     const Item it = item_at(w, i);
     if (it.split != 0 || it.parts <= 1) continue;
     const SeqInfo sq = w.seq[it.s];
+    const int rows = min(kPiece, sq.c * a.grp - it.tile * kItem - row0);
+    if (rows <= 0) continue;
     // the splits of a (tile, head) are nkv items apart
-    join<D>(a, sq, it.h, it.tile * kItem, min(kItem, sq.c * a.grp - it.tile * kItem), it.parts, nullptr,
-            [&](int k) { return a.part + (size_t)(i + k * w.nkv) * kItem * (D + 4); });
+    join<D>(a, sq, it.h, it.tile * kItem + row0, rows, it.parts, nullptr,
+            [&](int k) { return a.part + ((size_t)(i + k * w.nkv) * kItem + row0) * (D + 4); });
   }
 }
 
@@ -974,7 +996,7 @@ cudaError_t run(const PromptArgs& a, cudaStream_t st) {
   const long long items = a.b.n_seq * (long long)a.g.nkv * tiles * ((a.b.max_rows + kKeys - 1) / kKeys / kMinRun + 1);
   const int grid = (int)std::max<long long>(1, std::min<long long>(a.slots, items));
   if (cudaError_t e = launch(prompt_kernel<D, FP32, FEAT>, dim3(grid), kThreads, smem, st, false, a)) return e;
-  return launch(prompt_combine_kernel<D>, dim3((unsigned)a.slots), 512, (size_t)a.b.n_seq * sizeof(SeqInfo), st, true, a);
+  return launch(prompt_combine_kernel<D>, dim3((unsigned)(4 * a.slots)), 256, (size_t)a.b.n_seq * sizeof(SeqInfo), st, true, a);
 }
 
 }  // namespace

@@ -62,10 +62,12 @@ __device__ __forceinline__ void join(const Args& a, const SeqInfo& sq, int h, in
   for (int x = threadIdx.x; x < (items * sl + 31) / 32 * 32; x += blockDim.x) {
     const int item = min(x / sl, items - 1), k0 = x % sl, col = item / (D / 8), d0 = item % (D / 8) * 8;
     float m = -INFINITY;
+#pragma unroll 4
     for (int k = k0; k < n; k += sl) m = fmaxf(m, at(k)[col * kPart + D]);
     for (int i = 1; i < sl; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int k = k0; k < n; k += sl) {
       const float* p = at(k) + col * kPart;
       const float w = ex2(p[D] - base);
