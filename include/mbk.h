@@ -126,6 +126,19 @@ int mbk_create(const mbk_config *cfg, const mbk_weights *weights, void *kv_cache
 int mbk_create_paged(const mbk_config *cfg, const mbk_weights *weights, void *kv_pool, int32_t num_pages,
                      int32_t page_size, int device, mbk_handle **out);
 
+/* As mbk_create_paged, with the KV cache HELD IN 4 BITS: kv4_pool is a device pool in the format of "a KV
+ * cache held in 4 bits" below (mbk_kv4_pool_bytes of a configuration with this shape, num_pages,
+ * page_size, max_pages = kv_capacity / page_size rounded up, and track), 16-byte aligned.  Prompts and
+ * batches run on it: mbk_prefill (its pages set with mbk_set_page_table), mbk_batch_step and
+ * mbk_batch_step_kv4 quantise the new rows from fp32 and attend to the values that the rows stand for; with
+ * track = 1 each step adds to the rows' attention weights, so that mbk_kv4_evict can cut the sequences
+ * between steps.  The persistent decode kernel reads bf16 rows: mbk_decode_step, _steps, _greedy,
+ * _step_host and mbk_kv_fill return MBK_ERR_UNSUPPORTED on such a handle.
+ * Errors: as mbk_create, and MBK_ERR_INVALID_ARG for MBK_WEIGHTS_FP8 (the prompt path reads bf16 weights), a
+ * page_size that is not a power of two in [32, kv_capacity], num_pages < 1 or track not 0 or 1. */
+int mbk_create_kv4(const mbk_config *cfg, const mbk_weights *weights, void *kv4_pool, int32_t num_pages, int32_t page_size,
+                   int32_t track, int device, mbk_handle **out);
+
 /* FP8 copies of a bf16 matrix, exactly as mbk_create makes them for MBK_WEIGHTS_FP8: w (device bf16
  * [rows][cols], cols even) -> q (device [rows][cols] E4M3 codes) and s (device fp32 [rows] scales).
  * Asynchronous on `stream`.  Errors: MBK_ERR_INVALID_ARG for a NULL pointer, rows < 1 or an odd
@@ -231,6 +244,15 @@ int mbk_prefill(mbk_handle *h, const int32_t *tokens, int32_t n_tokens, int32_t 
  * logits_out while logits are asked for; as mbk_prefill otherwise.  Not yet run on a GPU. */
 int mbk_batch_step(mbk_handle *h, int32_t n_seq, const int32_t *counts, const int32_t *starts, const int32_t *tokens,
                    const int32_t *page_tables, float *logits_out, int32_t logits_mode, void *stream);
+
+/* mbk_batch_step on a tracked 4-bit pool whose sequences may have been cut (mbk_kv4_evict): sequence s
+ * holds held[s] <= starts[s] rows before the step (HOST array; the row counts that the eviction returned, plus the
+ * tokens of later steps), its tokens are at positions starts[s] .. and become rows held[s] .. .  A
+ * table's entries are read up to the last of these rows.  Errors: as mbk_batch_step, and
+ * MBK_ERR_INVALID_ARG for a handle that is not from mbk_create_kv4 with track = 1, NULL held, held[s]
+ * outside [0, starts[s]] or more than MBK_KV4_MAX_SEQS sequences. */
+int mbk_batch_step_kv4(mbk_handle *h, int32_t n_seq, const int32_t *counts, const int32_t *starts, const int32_t *held,
+                       const int32_t *tokens, const int32_t *page_tables, float *logits_out, int32_t logits_mode, void *stream);
 
 /* As mbk_decode_step, then copies the logits into the HOST buffer logits_host (vocab floats;
  * pinned memory makes the copy asynchronous) and synchronises `stream` before returning. */

@@ -54,6 +54,9 @@ struct mbk_handle {
   bool paged = false;
   int num_pages = 0, page_size = 0, max_pages = 0;
   int32_t* d_page_table = nullptr;
+  bool is_kv4 = false;  // mbk_create_kv4: the pool is held in 4 bits
+  Kv4Geom kv4{};
+  int num_sms = 0;
   // FP8 weights (MBK_WEIGHTS_FP8): the library's E4M3 copies and their per-row scales
   uint8_t* d_fp8 = nullptr;
   float* d_wscale = nullptr;
@@ -162,6 +165,8 @@ namespace {
 // The KV-cache layout of a handle: contiguous (num_pages == 0) or a pool of num_pages pages.
 struct KvLayout {
   int num_pages = 0, page_size = 0;
+  bool kv4 = false;
+  int track = 0;
 };
 int create_impl(const mbk_config* cfg, const mbk_weights* weights, void* kv_cache, KvLayout kvl, int device,
                 mbk_handle** out);
@@ -182,6 +187,25 @@ int mbk_create_paged(const mbk_config* cfg, const mbk_weights* weights, void* kv
   kvl.num_pages = num_pages;
   kvl.page_size = page_size;
   return create_impl(cfg, weights, kv_pool, kvl, device, out);
+}
+
+int mbk_create_kv4(const mbk_config* cfg, const mbk_weights* weights, void* kv4_pool, int32_t num_pages, int32_t page_size,
+                   int32_t track, int device, mbk_handle** out) {
+  if (!out) return MBK_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (config_check(cfg) != MBK_OK || cfg->weight_format != MBK_WEIGHTS_BF16 || page_size < 32 || page_size > cfg->kv_capacity)
+    return MBK_ERR_INVALID_ARG;
+  const mbk_kv4_config kc = {device, cfg->n_layers, cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, num_pages, page_size,
+                             (cfg->kv_capacity + page_size - 1) / page_size, track};
+  if (kv4_config_check(&kc) != MBK_OK) return MBK_ERR_INVALID_ARG;
+  KvLayout kvl;
+  kvl.num_pages = num_pages;
+  kvl.page_size = page_size;
+  kvl.kv4 = true;
+  kvl.track = track;
+  const int rc = create_impl(cfg, weights, kv4_pool, kvl, device, out);
+  if (rc == MBK_OK) (*out)->kv4 = kv4_geom(kc, kv4_pool);
+  return rc;
 }
 
 int mbk_quantize_fp8(const void* w, int32_t rows, int32_t cols, void* q, float* s, void* stream) {
@@ -233,6 +257,8 @@ int create_impl(const mbk_config* cfg, const mbk_weights* weights, void* kv_cach
   for (int l = 0; l < s.L; ++l)
     for (int k = 0; k < W_NSLOTS; ++k) h->bf16_layers[l].w[k] = reinterpret_cast<const uint16_t*>(wa.layers[l][k]);
   h->paged = kvl.num_pages > 0;
+  h->is_kv4 = kvl.kv4;
+  h->num_sms = prop.multiProcessorCount;
   h->num_pages = kvl.num_pages;
   h->page_size = kvl.page_size;
   h->max_pages = h->paged ? (cfg->kv_capacity + kvl.page_size - 1) / kvl.page_size : 0;
@@ -418,7 +444,7 @@ int create_impl(const mbk_config* cfg, const mbk_weights* weights, void* kv_cach
   // map cannot be made
   kp.attn_box_rows = std::min(kp.page_size, 64);
   const uint64_t kv_rows = h->paged ? (uint64_t)h->num_pages * (kp.page_elems / 64) : (uint64_t)s.L * 2 * s.nkv * s.C;
-  kp.attn_mma = p.attn_mma && make_kv_tile_map(&h->kvmap, kv_cache, kv_rows, (uint32_t)kp.attn_box_rows) ? 1 : 0;
+  kp.attn_mma = p.attn_mma && !kvl.kv4 && make_kv_tile_map(&h->kvmap, kv_cache, kv_rows, (uint32_t)kp.attn_box_rows) ? 1 : 0;
   kp.wbytes = s.wb;
   kp.wscale_layer = wscale_layer;
   kp.wscale = h->d_wscale;
@@ -473,6 +499,7 @@ int launch_steps(mbk_handle* h, int32_t token, const int32_t* d_tokens, int n, i
 
 int mbk_decode_step(mbk_handle* h, int32_t token_id, int32_t position, float* logits_out, void* stream) {
   if (!h || !logits_out) return MBK_ERR_INVALID_ARG;
+  if (h->is_kv4) return MBK_ERR_UNSUPPORTED;  // the decode kernel reads bf16 rows
   if (token_id < 0 || token_id >= h->cfg.vocab || position < 0 || position >= h->mapped) return MBK_ERR_INVALID_ARG;
   if (int st = sticky_status(h)) return st;
   if (cudaSetDevice(h->device) != cudaSuccess) return MBK_ERR_CUDA;
@@ -483,6 +510,7 @@ int mbk_decode_step(mbk_handle* h, int32_t token_id, int32_t position, float* lo
 int mbk_decode_steps(mbk_handle* h, const int32_t* tokens, int32_t n_steps, int32_t position, float* logits_out,
                      void* stream) {
   if (!h || !tokens || !logits_out || n_steps < 1) return MBK_ERR_INVALID_ARG;
+  if (h->is_kv4) return MBK_ERR_UNSUPPORTED;
   if (position < 0 || n_steps > h->mapped || position > h->mapped - n_steps) return MBK_ERR_INVALID_ARG;
   for (int32_t i = 0; i < n_steps; ++i)
     if (tokens[i] < 0 || tokens[i] >= h->cfg.vocab) return MBK_ERR_INVALID_ARG;
@@ -500,6 +528,7 @@ int mbk_decode_steps(mbk_handle* h, const int32_t* tokens, int32_t n_steps, int3
 int mbk_decode_greedy(mbk_handle* h, int32_t first_token, int32_t n_steps, int32_t position, int32_t* tokens_out,
                       float* logits_out, void* stream) {
   if (!h || !tokens_out || n_steps < 1) return MBK_ERR_INVALID_ARG;
+  if (h->is_kv4) return MBK_ERR_UNSUPPORTED;
   if (first_token < 0 || first_token >= h->cfg.vocab) return MBK_ERR_INVALID_ARG;
   if (position < 0 || n_steps > h->mapped || position > h->mapped - n_steps) return MBK_ERR_INVALID_ARG;
   if (h->inject_armed) return MBK_ERR_STATE;  // injection is defined for single teacher-forced steps only
@@ -543,6 +572,8 @@ int run_tokens(mbk_handle* h, const PrefillBatch& batch, const int32_t* tokens, 
   m.status = kp.status;
   m.host_status = kp.host_status;
   m.timeout_ns = kp.timeout_ns;
+  m.kv4 = h->is_kv4 ? &h->kv4 : nullptr;
+  m.num_sms = h->num_sms;
   const float* inject = h->prefill_inject_n != 0 ? h->d_prefill_inject : nullptr;
   h->prefill_inject_n = 0;  // one call
   return prefill_run(m, h->prefill, tokens, n, batch, logits_out, logits_mode, (cudaStream_t)stream, inject);
@@ -567,17 +598,20 @@ int mbk_prefill(mbk_handle* h, const int32_t* tokens, int32_t n_tokens, int32_t 
   return run_tokens(h, b, tokens, n_tokens, logits_out, logits_mode, stream);
 }
 
-int mbk_batch_step(mbk_handle* h, int32_t n_seq, const int32_t* counts, const int32_t* starts, const int32_t* tokens,
-                   const int32_t* page_tables, float* logits_out, int32_t logits_mode, void* stream) {
+namespace {
+// mbk_batch_step and mbk_batch_step_kv4 (held: cache rows before the step).
+int batch_step(mbk_handle* h, int32_t n_seq, const int32_t* counts, const int32_t* starts, const int32_t* held, const int32_t* tokens,
+               const int32_t* page_tables, float* logits_out, int32_t logits_mode, void* stream) {
   if (!h || n_seq < 1 || !counts || !starts || !tokens || !page_tables) return MBK_ERR_INVALID_ARG;
-  if (!h->paged || !logits_mode_ok(logits_mode, logits_out)) return MBK_ERR_INVALID_ARG;
+  if (!h->paged || !logits_mode_ok(logits_mode, logits_out) || (h->is_kv4 && n_seq > MBK_KV4_MAX_SEQS)) return MBK_ERR_INVALID_ARG;
   const int C = h->cfg.kv_capacity, ps = h->page_size;
   std::vector<char> used(h->num_pages, 0);
   int64_t n = 0;
   for (int32_t q = 0; q < n_seq; ++q) {
     if (counts[q] < 1 || starts[q] < 0 || counts[q] > C || starts[q] > C - counts[q]) return MBK_ERR_INVALID_ARG;
+    if (held && (held[q] < 0 || held[q] > starts[q])) return MBK_ERR_INVALID_ARG;
     const int32_t* t = page_tables + (size_t)q * h->max_pages;
-    const int need = (starts[q] + counts[q] + ps - 1) / ps;  // pages the sequence's positions reach
+    const int need = ((held ? held[q] : starts[q]) + counts[q] + ps - 1) / ps;  // pages the sequence's rows reach
     for (int i = 0; i < need; ++i) {
       if (t[i] < 0 || t[i] >= h->num_pages || used[t[i]]) return MBK_ERR_INVALID_ARG;  // in the pool, not shared
       used[t[i]] = 1;
@@ -593,7 +627,20 @@ int mbk_batch_step(mbk_handle* h, int32_t n_seq, const int32_t* counts, const in
   b.starts = starts;
   b.tables = page_tables;
   b.max_pages = h->max_pages;
+  b.held = held;
   return run_tokens(h, b, tokens, (int32_t)n, logits_out, logits_mode, stream);
+}
+}  // namespace
+
+int mbk_batch_step(mbk_handle* h, int32_t n_seq, const int32_t* counts, const int32_t* starts, const int32_t* tokens,
+                   const int32_t* page_tables, float* logits_out, int32_t logits_mode, void* stream) {
+  return batch_step(h, n_seq, counts, starts, nullptr, tokens, page_tables, logits_out, logits_mode, stream);
+}
+
+int mbk_batch_step_kv4(mbk_handle* h, int32_t n_seq, const int32_t* counts, const int32_t* starts, const int32_t* held,
+                       const int32_t* tokens, const int32_t* page_tables, float* logits_out, int32_t logits_mode, void* stream) {
+  if (!h || !held || !h->is_kv4 || !h->kv4.track) return MBK_ERR_INVALID_ARG;
+  return batch_step(h, n_seq, counts, starts, held, tokens, page_tables, logits_out, logits_mode, stream);
 }
 
 int mbk_debug_prefill_inject(mbk_handle* h, const float* x_in, int32_t n_tokens) {
@@ -631,6 +678,7 @@ int mbk_decode_step_host(mbk_handle* h, int32_t token_id, int32_t position, floa
 
 int mbk_kv_fill(mbk_handle* h, int layer, const float* k_raw, const float* v_raw, int32_t p0, int32_t n, void* stream) {
   if (!h || !k_raw || !v_raw) return MBK_ERR_INVALID_ARG;
+  if (h->is_kv4) return MBK_ERR_UNSUPPORTED;  // mbk_kv4_append stores rows there
   const mbk_config& c = h->cfg;
   if (layer < 0 || layer >= c.n_layers || p0 < 0 || n < 0 || (int64_t)p0 + n > h->mapped) return MBK_ERR_INVALID_ARG;
   if (int st = sticky_status(h)) return st;

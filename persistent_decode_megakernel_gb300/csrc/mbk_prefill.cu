@@ -412,7 +412,7 @@ __device__ __forceinline__ size_t kv_index(const KvGeom& g, const int32_t* table
 
 // Token t (position pos[t] of sequence seq[t]): rotate its q and k heads in place (rotate-half pairs
 // (i, i + d/2) by the angle of table row p), then store its K and V rows in its sequence's cache as
-// bf16 (nearest even).
+// bf16 (nearest even); without a bf16 cache (g.kv null) only rotate.
 __global__ void rope_kv_kernel(float* qkv, int ld, int n, const int32_t* pos, const int32_t* seq, int nq,
                                const float2* rope, KvGeom g, int layer) {
   const int d = g.d, half = d / 2, nkv = g.nkv;
@@ -429,12 +429,17 @@ __global__ void rope_kv_kernel(float* qkv, int ld, int n, const int32_t* pos, co
       v[i + half] = b * cs.x + a * cs.y;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 2 * nkv * d; e += blockDim.x) {
+    for (int e = threadIdx.x; g.kv != nullptr && e < 2 * nkv * d; e += blockDim.x) {
       const int sel = e / (nkv * d), rem = e - sel * nkv * d, h = rem / d, j = rem - h * d;
       g.kv[kv_index(g, table, layer, sel, h, p) + j] = to_bf16(row[(size_t)(nq + sel * nkv) * d + rem]);
     }
     __syncthreads();
   }
+}
+
+// x [n] fp32 split into (hi, lo).
+__global__ void split_kernel(const float* x, size_t n, uint16_t* hi, uint16_t* lo) {
+  for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (size_t)gridDim.x * blockDim.x) split_store(x[e], hi, lo, e);
 }
 
 // h = silu(gate) * up for gu [n][2I] (gate columns 0..I-1, up columns I..2I-1), split into (hi, lo).
@@ -959,7 +964,64 @@ void prefill_free(PrefillState& s) {
   if (s.tables != nullptr) cudaFree(s.tables);
   s.tables = nullptr;
   s.tables_cap = 0;
+  if (s.kv4_ws != nullptr) cudaFree(s.kv4_ws);
+  s.kv4_ws = nullptr;
+  s.kv4_cap = 0;
 }
+
+namespace {
+// What the layers' attention over a 4-bit cache takes, set up once per call.
+struct Kv4Step {
+  Kv4Batch batch;
+  float* out;  // [n][qd]
+  void* ws;
+};
+
+// Grows the 4-bit cache's workspace to this call and copies the batch's arrays to it.  tables: DEVICE.
+int prepare_kv4(const PrefillModel& m, PrefillState& s, int n, const PrefillBatch& b, const int32_t* tables, cudaStream_t st, Kv4Step* out) {
+  if (b.n_seq > kKv4MaxSeqs) return MBK_ERR_INVALID_ARG;
+  std::vector<int32_t> img;
+  img.reserve((size_t)3 * b.n_seq + 1);
+  int max_count = 1, max_rows = 1;
+  img.push_back(0);
+  for (int q = 0; q < b.n_seq; ++q) {
+    img.push_back(img.back() + b.counts[q]);
+    max_count = std::max(max_count, (int)b.counts[q]);
+  }
+  for (int q = 0; q < b.n_seq; ++q) {
+    img.push_back((b.held != nullptr ? b.held[q] : b.starts[q]) + b.counts[q]);
+    max_rows = std::max(max_rows, (int)img.back());
+  }
+  for (int q = 0; q < b.n_seq; ++q) img.push_back(b.starts[q]);
+  Kv4Batch& kb = out->batch;
+  kb.n_seq = b.n_seq;
+  kb.n_tokens = n;
+  kb.max_count = max_count;
+  kb.max_rows = max_rows;
+  const size_t qd = (size_t)m.nq * m.d;
+  const size_t b_int = round256(sizeof(int32_t) * img.size()), b_out = round256(sizeof(float) * (size_t)n * qd);
+  const size_t need = b_int + b_out + kv4_attention_workspace(*m.kv4, kb, m.num_sms);
+  if (need > s.kv4_cap) {
+    if (s.kv4_ws != nullptr) cudaFree(s.kv4_ws);
+    s.kv4_ws = nullptr;
+    s.kv4_cap = 0;
+    if (cudaMalloc(&s.kv4_ws, need) != cudaSuccess) return MBK_ERR_NOMEM;
+    s.kv4_cap = need;
+  }
+  unsigned char* w = reinterpret_cast<unsigned char*>(s.kv4_ws);
+  int32_t* ints = reinterpret_cast<int32_t*>(w);
+  if (cudaMemcpyAsync(ints, img.data(), sizeof(int32_t) * img.size(), cudaMemcpyHostToDevice, st) != cudaSuccess) return MBK_ERR_CUDA;
+  kb.offsets = ints;
+  kb.rows = ints + b.n_seq + 1;
+  kb.positions = m.kv4->track ? ints + 2 * b.n_seq + 1 : nullptr;  // an untracked cache was never cut: rows are positions
+  kb.tables = tables;
+  kb.status = reinterpret_cast<int32_t*>(m.status);  // a wait that gave up: MBK_KV4_TIMEOUT is DS_TIMEOUT
+  out->out = reinterpret_cast<float*>(w + b_int);
+  out->ws = w + b_int + b_out;
+  return MBK_OK;
+}
+static_assert(MBK_KV4_TIMEOUT == DS_TIMEOUT, "one status word for both");
+}  // namespace
 
 int prefill_run(const PrefillModel& m, PrefillState& s, const int32_t* tokens_host, int n, const PrefillBatch& batch,
                 float* logits, int mode, cudaStream_t st, const float* inject) {
@@ -1013,6 +1075,11 @@ int prefill_run(const PrefillModel& m, PrefillState& s, const int32_t* tokens_ho
     geom.tables = s.tables;
     geom.max_pages = batch.max_pages;
   }
+  Kv4Step kv4;
+  if (m.kv4 != nullptr) {
+    if (int rc = prepare_kv4(m, s, n, batch, geom.tables, st, &kv4)) return rc;
+    geom.kv = nullptr;
+  }
 
   const unsigned rows_grid = (unsigned)std::min(n, 4096);
   bool ok = true;
@@ -1034,7 +1101,15 @@ int prefill_run(const PrefillModel& m, PrefillState& s, const int32_t* tokens_ho
     ck(gemm(m, ah_H, al_H, qkv, 3, n, m.H, s.qkv, qkvd, 0, st));
     rope_kv_kernel<<<rows_grid, 256, 0, st>>>(s.qkv, qkvd, n, s.pos, s.seq, m.nq, m.rope, geom, l);
     ck(cudaGetLastError());
-    ck(attention(m, s, geom, l, ntiles, st));
+    if (m.kv4 != nullptr) {
+      Kv4Attn at{s.qkv, kv4.out, qkvd, qd, 0, m.attn_scale, 0.f, nullptr, 0, m.kv4->track};
+      ck(kv4_append(*m.kv4, l, kv4.batch, s.qkv + qd, s.qkv + qd + kvd, qkvd, 0, st));
+      ck(kv4_attention(*m.kv4, l, kv4.batch, at, kv4.ws, m.num_sms, st));
+      split_kernel<<<(unsigned)std::min<size_t>(1216, ((size_t)n * qd + 255) / 256), 256, 0, st>>>(kv4.out, (size_t)n * qd, s.a_hi, s.a_lo);
+      ck(cudaGetLastError());
+    } else {
+      ck(attention(m, s, geom, l, ntiles, st));
+    }
     const Seg o[1] = {{&lm[WM_O], m.H, 0, nullptr}};
     ck(gemm(m, ah_q, al_q, o, 1, n, qd, s.x, m.H, 1, st));
     // MLP sublayer

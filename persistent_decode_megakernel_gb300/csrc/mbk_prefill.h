@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "mbk_device.h"
+#include "mbk_kv4.h"
 
 namespace mbk {
 
@@ -32,6 +33,8 @@ struct PrefillModel {
   const int32_t* page_table;
   int page_size, page_shift;
   unsigned long long page_elems;
+  const Kv4Geom* kv4;           // a pool held in 4 bits instead of kv (paged: page_table), or null
+  int num_sms;
   unsigned* status;             // device status word [4] shared with the decode kernel
   unsigned* host_status;        // its mapped host copy (may be null)
   unsigned long long timeout_ns;
@@ -54,6 +57,9 @@ struct PrefillState {
   int2* tiles = nullptr;        // [cap] attention tiles: (first token, tokens) of one sequence
   int32_t* tables = nullptr;    // page tables of a batch of sequences (grown on demand)
   size_t tables_cap = 0;        // int32 entries allocated there
+  // a 4-bit cache: the batch's arrays [offsets | rows | positions], the attention's output and workspace
+  void* kv4_ws = nullptr;
+  size_t kv4_cap = 0;           // bytes allocated there
   std::vector<CUtensorMap> wmaps;  // per layer Wq, Wk, Wv, Wo, Wgate, Wup, Wdown; then E
   bool smem_set = false;
 };
@@ -68,6 +74,9 @@ struct PrefillBatch {
   const int32_t* starts = nullptr;
   const int32_t* tables = nullptr;
   int max_pages = 0;
+  // 4-bit cache: rows that the sequence's cache holds before the step (fewer than starts[s] once it has been
+  // cut), or null: starts
+  const int32_t* held = nullptr;
 };
 
 // Logits the caller asks for (values of the C ABI's MBK_PREFILL_LOGITS_*).

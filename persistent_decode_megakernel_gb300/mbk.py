@@ -30,7 +30,8 @@ EXPORTED = ("mbk_create", "mbk_decode_step", "mbk_decode_step_host", "mbk_kv_fil
             "mbk_trace_enable", "mbk_trace_read", "mbk_debug_inject", "mbk_decode_step_static", "mbk_decode_steps",
             "mbk_decode_greedy", "mbk_create_paged", "mbk_set_page_table", "mbk_quantize_fp8", "mbk_prefill",
             "mbk_debug_prefill_inject", "mbk_plan_simulate", "mbk_batch_step", "mbk_kv4_pool_bytes", "mbk_kv4_append",
-            "mbk_kv4_read", "mbk_kv4_attention_workspace", "mbk_kv4_attention", "mbk_kv4_evict_workspace", "mbk_kv4_evict")
+            "mbk_kv4_read", "mbk_kv4_attention_workspace", "mbk_kv4_attention", "mbk_kv4_evict_workspace", "mbk_kv4_evict",
+            "mbk_create_kv4", "mbk_batch_step_kv4")
 TASK_TYPES = {1: "qkv", 2: "attn", 3: "oproj", 4: "gateup", 5: "down", 6: "lmhead"}
 TRACE_STAMPS = 8  # per task: begin, inputs ready, end, first weight stage, four phase marks
 
@@ -155,6 +156,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.mbk_debug_inject.restype = ctypes.c_int
         lib.mbk_decode_step_static.argtypes = [ctypes.POINTER(MbkConfig), ctypes.POINTER(MbkWeights), vp, i32, i32, vp, vp]
         lib.mbk_decode_step_static.restype = ctypes.c_int
+        lib.mbk_create_kv4.argtypes = [ctypes.POINTER(MbkConfig), ctypes.POINTER(MbkWeights), vp, i32, i32, i32, ctypes.c_int,
+                                       ctypes.POINTER(vp)]
+        lib.mbk_create_kv4.restype = ctypes.c_int
+        lib.mbk_batch_step_kv4.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, i32, vp]
+        lib.mbk_batch_step_kv4.restype = ctypes.c_int
         i64, f32, kcfg, kbatch = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(MbkKv4Config), ctypes.POINTER(MbkKv4Batch)
         lib.mbk_kv4_pool_bytes.argtypes = [kcfg]
         lib.mbk_kv4_pool_bytes.restype = i64
@@ -233,6 +239,23 @@ def mbk_prefill(h, tokens, position: int, logits_ptr: int, logits_mode: int, str
     arr = np.ascontiguousarray(np.asarray(tokens, dtype=np.int32))
     return load_library().mbk_prefill(h, arr.ctypes.data_as(ctypes.c_void_p), int(arr.size), int(position),
                                       ctypes.c_void_p(logits_ptr or None), int(logits_mode), ctypes.c_void_p(stream_ptr))
+
+
+def mbk_batch_step_kv4(h, counts, starts, held, tokens, page_tables, logits_ptr: int, logits_mode: int, stream_ptr: int) -> int:
+    """As mbk_batch_step; held: rows that each sequence's cache holds before the step."""
+    import numpy as np
+    a = [np.ascontiguousarray(np.asarray(x, dtype=np.int32)) for x in (counts, starts, held, tokens, page_tables)]
+    vp = ctypes.c_void_p
+    return load_library().mbk_batch_step_kv4(h, int(a[0].size), *[x.ctypes.data_as(vp) for x in a], vp(logits_ptr or None),
+                                             int(logits_mode), vp(stream_ptr))
+
+
+def mbk_create_kv4(cfg: MbkConfig, weights: MbkWeights, kv4_pool_ptr: int, num_pages: int, page_size: int, track: bool,
+                   device: int) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    _check(load_library().mbk_create_kv4(ctypes.byref(cfg), ctypes.byref(weights), ctypes.c_void_p(kv4_pool_ptr), int(num_pages),
+                                         int(page_size), int(bool(track)), int(device), ctypes.byref(h)), "mbk_create_kv4")
+    return h
 
 
 def mbk_batch_step(h, counts, starts, tokens, page_tables, logits_ptr: int, logits_mode: int, stream_ptr: int) -> int:
@@ -364,10 +387,12 @@ class Decoder:
     step() launches one decode step into a device logits tensor on the current torch stream.
     """
 
-    def __init__(self, wl, device: int = 0, paged=None, fp8: bool = False):
+    def __init__(self, wl, device: int = 0, paged=None, fp8: bool = False, kv4: bool = False, track: bool = False):
         """paged: None for a contiguous cache, or (num_pages, page_size, pages): a pool of num_pages
         pages and the page table pages[q] for logical page q.  fp8: stream FP8 copies of the weights
-        (MBK_WEIGHTS_FP8)."""
+        (MBK_WEIGHTS_FP8).  kv4 (with paged): hold the pool in 4 bits (mbk_create_kv4), for prefill and
+        batch_step; `cache` is then its Kv4Cache, and with track its rows carry attention weights for
+        cache.evict."""
         import torch
         self.torch = torch
         s = wl.shape
@@ -378,7 +403,14 @@ class Decoder:
         self.final_norm = wl.final_norm.to(dev)
         self.layers = [{k: (None if v is None else v.to(dev)) for k, v in w.items()} for w in wl.layers]
         self.paged = paged
-        if paged is None:
+        self.cache = None
+        if kv4:
+            from .kv4 import Kv4Cache
+            if paged is None:
+                raise ValueError("kv4 needs paged")
+            self.cache = Kv4Cache(s.n_layers, s.n_heads, s.n_kv_heads, s.head_dim, paged[0], paged[1],
+                                  max_pages=-(-s.kv_capacity // paged[1]), track=track, device=device)
+        elif paged is None:
             self.kv = torch.zeros((s.n_layers, 2, s.n_kv_heads, s.kv_capacity, s.head_dim), dtype=torch.bfloat16, device=dev)
         else:
             num_pages, page_size, _ = paged
@@ -392,13 +424,16 @@ class Decoder:
         self._layer_arr = arr
         self.weights = MbkWeights(self.embed.data_ptr(), self.final_norm.data_ptr(), arr)
         self.cfg = config_from_shape(s, MBK_WEIGHTS_FP8 if fp8 else MBK_WEIGHTS_BF16)
-        if paged is None:
+        if kv4:
+            self.handle = mbk_create_kv4(self.cfg, self.weights, self.cache.pool.data_ptr(), paged[0], paged[1], track, device)
+            self.set_pages(paged[2])
+        elif paged is None:
             self.handle = mbk_create(self.cfg, self.weights, self.kv.data_ptr(), device)
         else:
             self.handle = mbk_create_paged(self.cfg, self.weights, self.pool.data_ptr(), paged[0], paged[1], device)
             self.set_pages(paged[2])
         self.logits = torch.empty(s.vocab, dtype=torch.float32, device=dev)
-        if s.prefill:
+        if s.prefill and not kv4:
             self.fill(wl.k_raw, wl.v_raw, 0)
 
     def set_pages(self, pages) -> None:
@@ -408,7 +443,9 @@ class Decoder:
 
     def logical_kv(self):
         """The cache in the contiguous layout [L][2][nkv][C][d] (paged: gathered through the page table;
-        unmapped positions read as zero)."""
+        unmapped positions read as zero).  Not for a 4-bit pool (cache.read)."""
+        if self.cache is not None:
+            raise ValueError("a 4-bit pool: use cache.read")
         if self.paged is None:
             return self.kv
         torch = self.torch
@@ -473,10 +510,11 @@ class Decoder:
                "mbk_prefill")
         return out
 
-    def batch_step(self, chunks, page_tables, logits: str = "last", out=None):
+    def batch_step(self, chunks, page_tables, logits: str = "last", out=None, held=None):
         """One step over several sequences of a paged decoder (mbk_batch_step): chunks = [(start,
         [tokens...]), ...], one per sequence; page_tables [n_seq][max_pages].  logits "last" ->
-        [n_seq, vocab], "all" -> [sum of tokens, vocab], None -> no logits."""
+        [n_seq, vocab], "all" -> [sum of tokens, vocab], None -> no logits.  held (a tracked 4-bit pool):
+        the rows that each sequence holds before the step, once it has been cut (mbk_batch_step_kv4)."""
         counts = [len(t) for _, t in chunks]
         starts = [p for p, _ in chunks]
         tokens = [x for _, t in chunks for x in t]
@@ -485,8 +523,11 @@ class Decoder:
             rows = len(chunks) if mode == 1 else len(tokens)
             out = self.torch.empty((rows, self.shape.vocab), dtype=self.torch.float32, device=self.device)
         stream = self.torch.cuda.current_stream(self.device).cuda_stream
-        _check(mbk_batch_step(self.handle, counts, starts, tokens, page_tables, out.data_ptr() if out is not None else 0,
-                              mode, stream), "mbk_batch_step")
+        ptr = out.data_ptr() if out is not None else 0
+        if held is not None:
+            _check(mbk_batch_step_kv4(self.handle, counts, starts, held, tokens, page_tables, ptr, mode, stream), "mbk_batch_step_kv4")
+        else:
+            _check(mbk_batch_step(self.handle, counts, starts, tokens, page_tables, ptr, mode, stream), "mbk_batch_step")
         return out
 
     def status(self) -> int:

@@ -120,3 +120,21 @@ def test_plain_format_pins():
     assert lo[0] == -65504 and scale[0] == np.float16(131008 / 15)
     assert plain.evict_map([5.0, 1.0, 3.0, 3.0, 0.0, 9.0], [0, 1, 2, 3, 4, 5], 3, 4) == [0, 4, 5]
     assert plain.evict_map([5.0, 1.0, 3.0, 3.0, 0.0], [0, 1, 2, 3, 9], 3, 9) == [0, 4, 2]
+
+
+def test_positions_need_a_tracked_pool(lib):
+    assert _append(lib, c=config(track=0), b=batch(positions=P)) == mbk.MBK_ERR_INVALID_ARG
+    assert _attention(lib, c=config(track=0), b=batch(positions=P)) == mbk.MBK_ERR_INVALID_ARG
+
+
+def test_4_bit_handles_are_refused_before_any_device_is_touched(lib):
+    from persistent_decode_megakernel_gb300 import workloads
+    h = ctypes.c_void_p()
+    cfg, w = mbk.config_from_shape(workloads.SHAPES["tiny"]), mbk.MbkWeights()
+    fp8 = mbk.config_from_shape(workloads.SHAPES["tiny"], mbk.MBK_WEIGHTS_FP8)
+    make = lambda c, pages, size, track: lib.mbk_create_kv4(ctypes.byref(c), ctypes.byref(w), P, pages, size, track, 0, ctypes.byref(h))  # noqa: E731
+    for c, pages, size, track in ((fp8, 4, 32, 0), (cfg, 0, 32, 0), (cfg, 4, 48, 0), (cfg, 4, 16, 0), (cfg, 4, 256, 0), (cfg, 4, 32, 2)):
+        assert make(c, pages, size, track) == mbk.MBK_ERR_INVALID_ARG and not h.value
+    assert lib.mbk_create_kv4(ctypes.byref(cfg), ctypes.byref(w), P, 4, 32, 0, 0, None) == mbk.MBK_ERR_INVALID_ARG
+    one = (ctypes.c_int32 * 1)(1)
+    assert lib.mbk_batch_step_kv4(None, 1, one, one, one, one, one, None, 0, None) == mbk.MBK_ERR_INVALID_ARG
