@@ -334,7 +334,7 @@ int mbk_decode_step_static(const mbk_config *cfg, const mbk_weights *weights, vo
  * read as zero, a bad sequence has no tokens) and OR a bit into *status. */
 
 #define MBK_KV4_MAX_SEQS 512  /* sequences of a call */
-#define MBK_KV4_MAX_EVICT_ROWS (1 << 20) /* rows of a sequence that is cut */
+#define MBK_KV4_MAX_EVICT_ROWS (1 << 19) /* rows of a sequence that is cut */
 #define MBK_KV4_BAD_PAGE 1    /* status bit: a page table entry outside [0, num_pages) */
 #define MBK_KV4_BAD_BATCH 2   /* status bit: rows, offsets or a token count outside their bounds */
 #define MBK_KV4_TIMEOUT 4     /* status bit: a wait inside the prompt kernel gave up after 2 s (outputs are invalid) */

@@ -6,8 +6,26 @@ namespace mbk {
 namespace {
 
 // ------------------------------------------------------------------ append and read
-// Eight lanes hold a group of 64, 8 elements each; a block of threads takes `per` tokens of one
-// sequence (grid.y).  Bound by the bytes: 8 n d elements read, 0.56 bytes written for each.
+// A row -- the K or V of one token and KV head -- is d / 8 lanes of 8 elements.  A CTA takes `per` tokens of one
+// sequence (grid.y), two rows per lane at a time.  Both are bound by the bytes once the instructions for an
+// element are few: no division by the number of heads (a multiplication by its reciprocal), codes through the low
+// bits of a large float or half instead of conversions (one in four clocks).
+struct RowsArgs {
+  Kv4Geom g;
+  Kv4Batch b;
+  int layer, per;
+  unsigned by_heads;  // ceil(2^32 / nkv), 0 for one head
+  long long ld;
+};
+struct RowAt {
+  int t, h, sel;
+};
+__device__ __forceinline__ RowAt row_at(const RowsArgs& a, int r) {  // r < 2 nkv per
+  const unsigned th = (unsigned)r >> 1;
+  const int t = a.by_heads == 0u ? (int)th : (int)__umulhi(th, a.by_heads);
+  return RowAt{t, (int)th - t * a.g.nkv, r & 1};
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -19,114 +37,151 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-// code = (x - lo) / scale to nearest even, in 0 .. 15.  The product with 1 / scale is within 2^-22 of
-// the quotient's 15 at most, so only a product nearer than 1e-5 to a half needs the division itself
-// (bf16 inputs do meet exact halves).
-__device__ __forceinline__ uint32_t code_of(float x, float lo, float scale, float inv) {
-  const float t = __fsub_rn(x, lo);
-  float q = __fmul_rn(t, inv);
-  const float h = q - floorf(q) - 0.5f;
-  if (fabsf(h) < 1e-5f) q = __fdiv_rn(t, scale);
-  return (uint32_t)fminf(fmaxf(rintf(q), 0.f), 15.f);
+// The codes of 8 elements: (x - lo) / scale to nearest even, in 0 .. 15.  The product with 1 / scale is within 2^-22
+// of the quotient's 15 at most, so only where one lies nearer than 1e-5 to a half the divisions themselves are made
+// (bf16 inputs do meet exact halves).  Adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low bits.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float lo, float scale, float inv) {
+  constexpr float kBig = 12582912.f;
+  float q[8], far = 0.f;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], lo), inv), 0.f), 15.f);
+    const float r = __fadd_rn(q[i], kBig);
+    far = fmaxf(far, fabsf(__fsub_rn(q[i], __fsub_rn(r, kBig))));
+    w |= (__float_as_uint(r) & 15u) << (4 * i);
+  }
+  if (far > 0.49999f) {
+    w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], lo), scale)), 0.f), 15.f) << (4 * i);
+  }
+  return w;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) append_kernel(Kv4Geom g, int layer, Kv4Batch b, const T* k, const T* v, long long ld, int per) {
-  const int s = blockIdx.y;
-  const SeqView q = seq_view(g, b, s, threadIdx.x == 0 && blockIdx.x == 0);
-  const int t0 = blockIdx.x * per;
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ RowsArgs a, const T* k, const T* v) {
+  constexpr int V = D / 8, kStep = 256 / V;  // lanes of a row, rows of a step
+  const Kv4Geom& g = a.g;
+  const int s = blockIdx.y, t0 = blockIdx.x * a.per;
+  const SeqView q = seq_view(g, a.b, s, threadIdx.x == 0 && blockIdx.x == 0);
   if (t0 >= q.c) return;
   if (q.r < q.c) {
-    if (threadIdx.x == 0) flag(b.status, MBK_KV4_BAD_BATCH);
+    if (threadIdx.x == 0) flag(a.b.status, MBK_KV4_BAD_BATCH);
     return;
   }
-  const int nt = min(per, q.c - t0);
-  const int32_t* table = b.tables + (size_t)s * g.max_pages;
-  constexpr int V = D / 8;  // vectors of 8 in a row
-  const int work = nt * g.nkv * 2 * V;
-  const int p0 = b.positions != nullptr ? b.positions[s] : q.r - q.c;
-  for (int e = threadIdx.x; e < (work + 31) / 32 * 32; e += blockDim.x) {
-    const bool on = e < work;  // groups of 8 lanes are all on or all off
-    const int ee = on ? e : 0;
-    const int j = ee % V, hv = ee / V, sel = hv & 1, th = hv >> 1, h = th % g.nkv, t = t0 + th / g.nkv;
-    float x[8];
-    load8<T>((sel ? v : k) + (size_t)(q.tok0 + t) * ld + h * D + 8 * j, x);
-    float lo = INFINITY, hi = -INFINITY;
+  const int rows = min(a.per, q.c - t0) * g.nkv * 2, j = threadIdx.x % V, first = threadIdx.x / V;
+  const int32_t* table = a.b.tables + (size_t)s * g.max_pages;
+  const int p0 = a.b.positions != nullptr ? a.b.positions[s] : q.r - q.c;
+  for (int r0 = 0; r0 < rows; r0 += 2 * kStep) {  // all lanes of a warp go round together
+    RowAt at[2];
+    float x[2][8];
+    bool on[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = x[i] != x[i] ? x[i] : fminf(fmaxf(x[i], -65504.f), 65504.f);
-      lo = min_nan(lo, x[i]);
-      hi = max_nan(hi, x[i]);
+    for (int u = 0; u < 2; ++u) {
+      const int r = r0 + u * kStep + first;
+      on[u] = r < rows;
+      at[u] = row_at(a, on[u] ? r : 0);
+      at[u].t += t0;
+      load8<T>((at[u].sel ? v : k) + (size_t)(q.tok0 + at[u].t) * a.ld + at[u].h * D + 8 * j, x[u]);
     }
 #pragma unroll
-    for (int m = 1; m < 8; m <<= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    }
-    const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), lh = __float2half_rn(lo);
-    const float sf = __half2float(sh), lf = __half2float(lh);
-    uint32_t w = 0;
-    if (sf > 0.f) {  // a constant group, and one with a NaN, has codes of zero
-      const float inv = __fdiv_rn(1.f, sf);
+    for (int u = 0; u < 2; ++u) {
+      float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w |= code_of(x[i], lf, sf, inv) << (4 * i);
-    }
-    if (!on) continue;
-    const int row = q.r - q.c + t, lane_row = row % kRows;
-    uint8_t* blk = block_of(g, table, layer, h, row, b.status);
-    if (blk == nullptr) continue;
-    uint8_t* base = blk + sel * half_bytes(D);
-    *reinterpret_cast<uint32_t*>(base + lane_row * (D / 2) + 4 * j) = w;
-    if (j % 8 == 0) {
-      const __half2 p = __halves2half2(sh, lh);
-      *reinterpret_cast<__half2*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 8) * 4) = p;
-    }
-    if (g.track && sel == 0 && j == 0) {
-      *reinterpret_cast<int32_t*>(blk + pos_at(D) + 4 * lane_row) = p0 + t;
-      *reinterpret_cast<float*>(blk + weight_at(D) + 4 * lane_row) = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        lo = min_nan(lo, x[u][i]);
+        hi = max_nan(hi, x[u][i]);
+      }
+#pragma unroll
+      for (int m = 1; m < 8; m <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+      }
+      if (!(lo >= -65504.f && hi <= 65504.f)) {  // beyond fp16, or NaN, which stays
+        lo = lo != lo ? lo : fminf(fmaxf(lo, -65504.f), 65504.f);
+        hi = hi != hi ? hi : fminf(fmaxf(hi, -65504.f), 65504.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = fminf(fmaxf(x[u][i], -65504.f), 65504.f);
+      }
+      const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), lh = __float2half_rn(lo);
+      const float sf = __half2float(sh), lf = __half2float(lh);
+      // a constant group, and one with a NaN, has codes of zero
+      const uint32_t w = sf > 0.f ? codes_of(x[u], lf, sf, __fdiv_rn(1.f, sf)) : 0u;
+      if (!on[u]) continue;
+      const int row = q.r - q.c + at[u].t, lane_row = row % kRows;
+      uint8_t* blk = block_of(g, table, a.layer, at[u].h, row, a.b.status);
+      if (blk == nullptr) continue;
+      uint8_t* base = blk + at[u].sel * half_bytes(D);
+      *reinterpret_cast<uint32_t*>(base + lane_row * (D / 2) + 4 * j) = w;
+      if (j % 8 == 0)
+        *reinterpret_cast<__half2*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 8) * 4) = __halves2half2(sh, lh);
+      if (g.track && at[u].sel == 0 && j == 0) {
+        *reinterpret_cast<int32_t*>(blk + pos_at(D) + 4 * lane_row) = p0 + at[u].t;
+        *reinterpret_cast<float*>(blk + weight_at(D) + 4 * lane_row) = 0.f;
+      }
     }
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) read_kernel(Kv4Geom g, int layer, Kv4Batch b, T* k, T* v, long long ld, int per) {
-  const int s = blockIdx.y;
-  const SeqView q = seq_view(g, b, s, threadIdx.x == 0 && blockIdx.x == 0);
-  const int t0 = blockIdx.x * per;
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ RowsArgs a, T* k, T* v) {
+  constexpr int V = D / 8, kStep = 256 / V, kAtOnce = 4;
+  const Kv4Geom& g = a.g;
+  const int s = blockIdx.y, t0 = blockIdx.x * a.per;
+  const SeqView q = seq_view(g, a.b, s, threadIdx.x == 0 && blockIdx.x == 0);
   if (t0 >= q.c) return;
   if (q.r < q.c) {
-    if (threadIdx.x == 0) flag(b.status, MBK_KV4_BAD_BATCH);
+    if (threadIdx.x == 0) flag(a.b.status, MBK_KV4_BAD_BATCH);
     return;
   }
-  const int nt = min(per, q.c - t0);
-  const int32_t* table = b.tables + (size_t)s * g.max_pages;
-  constexpr int V = D / 8;
-  const int work = nt * g.nkv * 2 * V;
-  for (int e = threadIdx.x; e < work; e += blockDim.x) {
-    const int j = e % V, hv = e / V, sel = hv & 1, th = hv >> 1, h = th % g.nkv, t = t0 + th / g.nkv;
-    const int row = q.r - q.c + t, lane_row = row % kRows;
-    const uint8_t* blk = block_of(g, table, layer, h, row, b.status);
-    float x[8];
-    if (blk == nullptr) {
+  const int rows = min(a.per, q.c - t0) * g.nkv * 2, j = threadIdx.x % V, first = threadIdx.x / V;
+  const int32_t* table = a.b.tables + (size_t)s * g.max_pages;
+  for (int r0 = 0; r0 < rows; r0 += kAtOnce * kStep) {
+    uint32_t w[kAtOnce], pr[kAtOnce];
+    size_t to[kAtOnce];
+    int sel[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    } else {
-      const uint8_t* base = blk + sel * half_bytes(D);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(base + lane_row * (D / 2) + 4 * j);
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 8) * 4));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(p.x, (float)((w >> (4 * i)) & 15u), p.y);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int r = r0 + u * kStep + first;
+      sel[u] = -1;
+      if (r >= rows) continue;
+      RowAt at = row_at(a, r);
+      at.t += t0;
+      const int row = q.r - q.c + at.t, lane_row = row % kRows;
+      const uint8_t* blk = block_of(g, table, a.layer, at.h, row, a.b.status);
+      const uint8_t* base = blk + at.sel * half_bytes(D);
+      sel[u] = at.sel;
+      to[u] = (size_t)(q.tok0 + at.t) * a.ld + at.h * D + 8 * j;
+      w[u] = pr[u] = 0u;  // a bad page reads as zero
+      if (blk != nullptr) {
+        w[u] = __ldg(reinterpret_cast<const uint32_t*>(base + lane_row * (D / 2) + 4 * j));
+        pr[u] = __ldg(reinterpret_cast<const uint32_t*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 8) * 4));
+      }
     }
-    store8((sel ? v : k) + (size_t)(q.tok0 + t) * ld + h * D + 8 * j, x);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (sel[u] < 0) continue;
+      const float2 p = unpack_half(pr[u]);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // codes i and i + 4 as 1024 + code in fp16
+        const uint32_t c = (w[u] >> (4 * i) & 0x000f000fu) | 0x64006400u;
+        const float2 f = __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1024.f)));
+        x[i] = fmaf(p.x, f.x, p.y);
+        x[i + 4] = fmaf(p.x, f.y, p.y);
+      }
+      store8((sel[u] ? v : k) + to[u], x);
+    }
   }
 }
 
 // ------------------------------------------------------------------ eviction
-// select_kernel, one CTA per (layer, sequence, KV head): the keep-th largest key by radix selection
-// (keys: the order of the weights, the recent rows above all), equal keys lowest row first; then the
-// map: dest row j < keep takes row map[j] -- itself if it is kept, else the next kept row from above.
-constexpr int kSelThreads = 1024;
-constexpr int kKeysInSmem = 40960;
+// select_kernel, one CTA per (layer, sequence, KV head): the keep-th largest key by radix selection (keys: the order
+// of the weights, the recent rows above all), equal keys lowest row first; then the map: dest row j < keep takes row
+// map[j] -- itself if it is kept, else the next kept row from above.  Bound by its chain of passes and barriers
+// rather than by bytes, so short sequences take a small CTA, whose barriers cost less.
+constexpr int kKeysInSmem = 32768;
 
 __device__ __forceinline__ uint32_t weight_key(float w, int pos, int young) {
   if (pos >= young) return 0xffffffffu;
@@ -146,6 +201,7 @@ struct EvictArgs {
   int32_t* kept;    // [segment] rows that are left
 };
 
+template <int NT>
 __device__ int block_sum_scan(int v, int* sums, int* total) {  // exclusive scan over the block; all threads call
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -157,28 +213,25 @@ __device__ int block_sum_scan(int v, int* sums, int* total) {  // exclusive scan
   __syncthreads();
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int t = sums[lane];
+  int t = lane < NT / 32 ? sums[lane] : 0;  // every warp scans the warps' sums for itself
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, t, m);
-      if (lane >= m) t += y;
-    }
-    sums[lane] = t;
+  for (int m = 1; m < 32; m <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, t, m);
+    if (lane >= m) t += y;
   }
-  __syncthreads();
-  *total = sums[31];
-  return x - v + (warp > 0 ? sums[warp - 1] : 0);
+  *total = __shfl_sync(0xffffffffu, t, 31);
+  return x - v + (warp > 0 ? __shfl_sync(0xffffffffu, t, warp - 1) : 0);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictArgs a) {
+template <int D, int NT>
+__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int hist[2048];
   __shared__ int sums[32];
-  __shared__ int s_bin, s_above;
+  __shared__ int s_bin, s_above, s_in;
   const int seg = blockIdx.x, h = seg % a.g.nkv, s = seg / a.g.nkv % a.n_seq, layer = a.layer0 + seg / (a.g.nkv * a.n_seq);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int r = a.rows[s];
   if (r < 0 || r > a.max_rows) {
     if (tid == 0) flag(a.status, MBK_KV4_BAD_BATCH);
@@ -188,132 +241,186 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   int32_t* map = a.map + (size_t)seg * keep;
   if (tid == 0) a.kept[seg] = min(r, keep);
   if (r <= keep) {
-    for (int i = tid; i < r; i += kSelThreads) map[i] = i;
+    for (int i = tid; i < r; i += NT) map[i] = i;
     return;
   }
   const int32_t* table = a.tables + (size_t)s * a.g.max_pages;
   const int young = a.next_pos[s] - a.recent;
-  const int words = (r + 31) / 32;
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem);                 // kept rows
-  uint32_t* keys = bits + (a.max_rows + 31) / 32;                     // [r] when they fit
+  const int words = (r + 31) / 32, all_words = (a.max_rows + 31) / 32;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem);             // kept rows
+  int* ranks = reinterpret_cast<int*>(bits + all_words);          // [all_words + 1] free rows (kept rows from `keep` on) before a word
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ranks + all_words + 1);  // [r] when they fit
   const bool cached = a.max_rows <= kKeysInSmem;
   auto load_key = [&](int row) -> uint32_t {
     const uint8_t* p = block_of(a.g, table, layer, h, row, a.status);
     if (p == nullptr) return 0u;
-    return weight_key(*reinterpret_cast<const float*>(p + weight_at(D) + 4 * (row % kRows)),
-                      *reinterpret_cast<const int*>(p + pos_at(D) + 4 * (row % kRows)), young);
+    return weight_key(__ldg(reinterpret_cast<const float*>(p + weight_at(D) + 4 * (row % kRows))),
+                      __ldg(reinterpret_cast<const int*>(p + pos_at(D) + 4 * (row % kRows))), young);
   };
-  if (cached)
-    for (int i = tid; i < r; i += kSelThreads) keys[i] = load_key(i);
+  if (cached) {
+    for (int i0 = tid; i0 < r; i0 += 4 * NT) {
+      uint32_t k[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) k[u] = i0 + u * NT < r ? load_key(i0 + u * NT) : 0u;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * NT < r) keys[i0 + u * NT] = k[u];
+    }
+  }
   auto key = [&](int row) { return cached ? keys[row] : load_key(row); };
   // digits of 11, 11 and 10 bits from the top
   uint32_t prefix = 0, mask = 0;
   int need = keep;  // rows still to be taken from those that share the prefix
-  const int shift[3] = {21, 10, 0}, width[3] = {2048, 2048, 1024};
   for (int pass = 0; pass < 3; ++pass) {
-    for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 1024 : 2048;
+    for (int i = tid; i < 2048; i += NT) hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < r; i += kSelThreads) {
+    for (int i = tid; i < r; i += NT) {
       const uint32_t k = key(i);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift[pass]) & (width[pass] - 1)], 1);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (width - 1)], 1);
     }
     __syncthreads();
-    // thread t holds bins from the top: 2047 - 2 t and 2046 - 2 t
-    const int b0 = 2047 - 2 * tid, h0 = hist[b0], h1 = hist[b0 - 1];
+    // thread t holds kBins bins from the top: 2047 - kBins t and below
+    constexpr int kBins = 2048 / NT;
+    int n[kBins], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBins; ++i) sum += n[i] = hist[2047 - kBins * tid - i];
     int total;
-    const int above = block_sum_scan(h0 + h1, sums, &total);
-    if (above < need && above + h0 >= need) {
-      s_bin = b0;
-      s_above = above;
-    } else if (above + h0 < need && above + h0 + h1 >= need) {
-      s_bin = b0 - 1;
-      s_above = above + h0;
+    int above = block_sum_scan<NT>(sum, sums, &total);
+#pragma unroll
+    for (int i = 0; i < kBins; ++i) {
+      if (above < need && above + n[i] >= need) {
+        s_bin = 2047 - kBins * tid - i;
+        s_above = above;
+        s_in = n[i];
+      }
+      above += n[i];
     }
     __syncthreads();
-    prefix |= (uint32_t)s_bin << shift[pass];
-    mask |= (uint32_t)(width[pass] - 1) << shift[pass];
+    prefix |= (uint32_t)s_bin << shift;
+    mask |= (uint32_t)(width - 1) << shift;
     need -= s_above;
-    __syncthreads();
-  }
-  // rows above the threshold, and the first `need` rows equal to it
-  int taken = 0;
-  for (int i0 = 0; i0 < r; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < r ? key(i) : 0u;
-    const bool eq = i < r && k == prefix;
-    int total;
-    const int before = taken + block_sum_scan(eq ? 1 : 0, sums, &total);
-    const bool take = i < r && (k > prefix || (eq && before < need));
-    const uint32_t b = __ballot_sync(0xffffffffu, take);
-    if ((tid & 31) == 0 && i / 32 < words) bits[i / 32] = b;
-    taken += total;
-  }
-  __syncthreads();
-  // kept rows from `keep` on, in order
-  int32_t* movers = a.movers + (size_t)seg * keep;
-  int done = 0;
-  for (int w0 = keep / 32; w0 < words; w0 += kSelThreads) {
-    const int w = w0 + tid;
-    uint32_t b = w < words ? bits[w] : 0u;
-    if (w == keep / 32) b &= ~0u << (keep % 32);
-    int total;
-    int at = done + block_sum_scan(__popc(b), sums, &total);
-    for (; b != 0u; b &= b - 1) movers[at++] = w * 32 + __ffs(b) - 1;
-    done += total;
-  }
-  __syncthreads();
-  done = 0;
-  const int kw = (keep + 31) / 32;
-  for (int w0 = 0; w0 < kw; w0 += kSelThreads) {
-    const int w = w0 + tid;
-    uint32_t b = 0u, in = 0u;
-    if (w < kw) {
-      in = w == keep / 32 ? (1u << (keep % 32)) - 1u : ~0u;
-      b = ~bits[w] & in;
+    if (s_in == need) {  // all that share the prefix are taken: nothing more to tell apart (a key of 0 ends this too)
+      if (prefix != 0u) {
+        prefix -= 1u;
+        need = 0;
+        break;
+      }
     }
-    int total;
-    int at = done + block_sum_scan(__popc(b), sums, &total);
-    if (w < kw)
-      for (int i = 0; i < 32; ++i)
-        if (in >> i & 1u) map[w * 32 + i] = (b >> i & 1u) ? movers[at++] : w * 32 + i;
-    done += total;
+  }
+  // Rows above the threshold, and the first `need` rows equal to it.  Each warp has a run of whole words of rows, so that
+  // one scan over the warps' counts is enough.
+  const int per = (words + NT / 32 - 1) / (NT / 32), w_from = min(words, warp * per), w_to = min(words, w_from + per);
+  int before = 0;
+  if (need > 0) {
+    int equal = 0, all;
+    for (int w = w_from; w < w_to; ++w) {
+      const int i = w * 32 + lane;
+      equal += __popc(__ballot_sync(0xffffffffu, i < r && key(i) == prefix));
+    }
+    before = block_sum_scan<NT>(lane == 0 ? equal : 0, sums, &all);
+    before = __shfl_sync(0xffffffffu, before, 0);
+  }
+  // and in the same walk the free rows below `keep` (the kept ones above) before each word, from the warp's first on
+  int free_rows = 0, moved = 0;
+  for (int w = w_from; w < w_to; ++w) {
+    const int i = w * 32 + lane;
+    const uint32_t k = i < r ? key(i) : 0u;
+    const uint32_t eq = __ballot_sync(0xffffffffu, i < r && k == prefix);
+    const bool mine = (eq >> lane & 1u) && before + __popc(eq & ((1u << lane) - 1u)) < need;
+    const uint32_t b = __ballot_sync(0xffffffffu, mine || (i < r && k > prefix));
+    before += __popc(eq);
+    const uint32_t below = w < keep / 32 ? ~0u : w == keep / 32 ? (1u << (keep % 32)) - 1u : 0u;  // rows < keep of the word
+    if (lane == 0) {
+      bits[w] = b;
+      if (below != 0u) ranks[w] = free_rows;       // words up to keep / 32
+      if (below != ~0u) ranks[w + 1] = moved;      // words from keep / 32 on, one place further
+    }
+    free_rows += __popc(~b & below);
+    moved += __popc(b & ~below);
+  }
+  int total;
+  const int free_base = __shfl_sync(0xffffffffu, block_sum_scan<NT>(lane == 0 ? free_rows : 0, sums, &total), 0);
+  const int moved_base = __shfl_sync(0xffffffffu, block_sum_scan<NT>(lane == 0 ? moved : 0, sums, &total), 0);
+  for (int w = w_from + lane; w < w_to; w += 32) {
+    if (w * 32 < keep) ranks[w] += free_base;
+    if (w >= keep / 32) ranks[w + 1] += moved_base;
+  }
+  __syncthreads();
+  int32_t* movers = a.movers + (size_t)seg * keep;  // kept rows from `keep` on, in order
+  for (int i = keep + tid; i < r; i += NT) {
+    const uint32_t b = bits[i / 32] & (i / 32 == keep / 32 ? ~0u << (keep % 32) : ~0u);
+    if (b >> (i % 32) & 1u) movers[ranks[i / 32 + 1] + __popc(b & ((1u << (i % 32)) - 1u))] = i;
+  }
+  __syncthreads();
+  for (int j = tid; j < keep; j += NT) {
+    const uint32_t free_bits = ~bits[j / 32];
+    map[j] = free_bits >> (j % 32) & 1u ? movers[ranks[j / 32] + __popc(free_bits & ((1u << (j % 32)) - 1u))] : j;
   }
 }
 
-// move_kernel: 32 destination rows of a segment per CTA.  In place (no out_tables) a kept row below
-// `keep` stays and the others come from rows >= keep, so no row is both read and written.
+// move_kernel: kMove destination rows of a segment per CTA.  First where each row comes from (map, page table), then
+// the bytes, 16 at a time, several copies under way per thread.  In place (no out_tables) a kept row below `keep`
+// stays and the others come from rows >= keep, so no row is both read and written.
+constexpr int kMove = 128;
 template <int D>
 __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ EvictArgs a) {
-  const int nb = (min(a.keep, a.max_rows) + kRows - 1) / kRows, seg = blockIdx.x / nb, rb = blockIdx.x - seg * nb;
+  __shared__ const uint8_t* from[kMove];  // block of the source row, or null: nothing to move
+  __shared__ uint8_t* to[kMove];
+  __shared__ unsigned char lane_of[kMove];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int nb = (min(a.keep, a.max_rows) + kMove - 1) / kMove, seg = blockIdx.x / nb, rb = blockIdx.x - seg * nb;
   const int h = seg % a.g.nkv, s = seg / a.g.nkv % a.n_seq, layer = a.layer0 + seg / (a.g.nkv * a.n_seq);
-  const int n = a.kept[seg], r0 = rb * kRows;
+  const int n = a.kept[seg], r0 = rb * kMove;
   if (rb == 0 && h == 0 && layer == a.layer0 && threadIdx.x == 0) a.rows_out[s] = n;
   if (r0 >= n) return;
-  const bool in_place = a.out_tables == nullptr;
-  const int32_t* table = a.tables + (size_t)s * a.g.max_pages;
-  const int32_t* to = in_place ? table : a.out_tables + (size_t)s * a.out_pages;
-  const int32_t* map = a.map + (size_t)seg * a.keep;
-  uint8_t* dst = block_of(a.g, to, layer, h, r0, threadIdx.x == 0 ? a.status : nullptr);
-  if (dst == nullptr) return;
-  constexpr int C = D / 32;  // 16-byte chunks of a row's codes
-  const int rows = min(kRows, n - r0);
-  for (int i = threadIdx.x; i < rows * 2 * (C + 1); i += blockDim.x) {
-    const int row = i / (2 * (C + 1)), part = i % (2 * (C + 1)), sel = part / (C + 1), c = part % (C + 1);
-    const int src = map[r0 + row];
-    if (in_place && src == r0 + row) continue;
-    const uint8_t* from = block_of(a.g, table, layer, h, src, a.status);
-    if (from == nullptr) continue;
-    const int fr = src % kRows;
-    const uint8_t* f = from + sel * half_bytes(D);
-    uint8_t* d = dst + sel * half_bytes(D);
-    if (c < C) {
-      *reinterpret_cast<uint4*>(d + row * (D / 2) + 16 * c) = *reinterpret_cast<const uint4*>(f + fr * (D / 2) + 16 * c);
-    } else {
+  const int rows = min(kMove, n - r0);
+  if (threadIdx.x < rows) {
+    const bool in_place = a.out_tables == nullptr;
+    const int32_t* table = a.tables + (size_t)s * a.g.max_pages;
+    const int32_t* out = in_place ? table : a.out_tables + (size_t)s * a.out_pages;
+    const int row = r0 + threadIdx.x, src = a.map[(size_t)seg * a.keep + row];
+    const uint8_t* f = in_place && src == row ? nullptr : block_of(a.g, table, layer, h, src, a.status);
+    uint8_t* d = f == nullptr ? nullptr : block_of(a.g, out, layer, h, row, a.status);
+    from[threadIdx.x] = d == nullptr ? nullptr : f;
+    to[threadIdx.x] = d;
+    lane_of[threadIdx.x] = (unsigned char)(src % kRows);
+  }
+  __syncthreads();
+  constexpr int C = D / 32, kAtOnce = 4;  // 16-byte chunks of a row's codes
+  // codes: rows x (K, V) x C chunks
+  for (int i0 = threadIdx.x; i0 < rows * 2 * C; i0 += 256 * kAtOnce) {
+    uint4 x[kAtOnce];
 #pragma unroll
-      for (int g = 0; g < D / 64; ++g)
-        reinterpret_cast<uint32_t*>(d + code_bytes(D))[row * (D / 64) + g] = reinterpret_cast<const uint32_t*>(f + code_bytes(D))[fr * (D / 64) + g];
-      const int at = sel ? weight_at(D) : pos_at(D);
-      reinterpret_cast<uint32_t*>(dst + at)[row] = reinterpret_cast<const uint32_t*>(from + at)[fr];
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + 256 * u, row = i / (2 * C), sel = i / C % 2, c = i % C;
+      if (i < rows * 2 * C && from[row] != nullptr)
+        x[u] = __ldg(reinterpret_cast<const uint4*>(from[row] + sel * half_bytes(D) + lane_of[row] * (D / 2) + 16 * c));
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + 256 * u, row = i / (2 * C), sel = i / C % 2, c = i % C;
+      if (i < rows * 2 * C && from[row] != nullptr)
+        *reinterpret_cast<uint4*>(to[row] + sel * half_bytes(D) + (r0 + row) % kRows * (D / 2) + 16 * c) = x[u];
+    }
+  }
+  // pairs of K and V, position, weight: 4 bytes each
+  constexpr int G = D / 64, P = 2 * G + 2;
+  for (int i0 = threadIdx.x; i0 < rows * P; i0 += 256 * kAtOnce) {
+    uint32_t x[kAtOnce];
+    auto place = [&](int part, int lane) {  // byte of part `part` of row `lane` in its block
+      return part < 2 * G ? part / G * half_bytes(D) + code_bytes(D) + (lane * G + part % G) * 4
+                          : (part == 2 * G ? pos_at(D) : weight_at(D)) + 4 * lane;
+    };
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + 256 * u, row = i / P;
+      if (i < rows * P && from[row] != nullptr) x[u] = *reinterpret_cast<const uint32_t*>(from[row] + place(i % P, lane_of[row]));
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + 256 * u, row = i / P;
+      if (i < rows * P && from[row] != nullptr) *reinterpret_cast<uint32_t*>(to[row] + place(i % P, (r0 + row) % kRows)) = x[u];
     }
   }
 }
@@ -330,37 +437,62 @@ size_t kv4_evict_workspace(const Kv4Geom& g, int n_layers, int n_seq, int keep) 
   return 2 * round256(segs * keep * 4) + round256(segs * 4);
 }
 
+namespace {
+RowsArgs rows_args(const Kv4Geom& g, int layer, const Kv4Batch& b, long long ld) {
+  RowsArgs a;
+  a.g = g;
+  a.b = b;
+  a.layer = layer;
+  a.per = tokens_per_cta(g);
+  a.by_heads = g.nkv == 1 ? 0u : (unsigned)(((1ull << 32) + g.nkv - 1) / g.nkv);
+  a.ld = ld;
+  return a;
+}
+dim3 rows_grid(const RowsArgs& a) { return dim3((unsigned)((a.b.max_count + a.per - 1) / a.per), (unsigned)a.b.n_seq); }
+}  // namespace
+
 cudaError_t kv4_append(const Kv4Geom& g, int layer, const Kv4Batch& b, const void* k, const void* v, long long ld, int bf16,
                        cudaStream_t st) {
-  const int per = tokens_per_cta(g);
-  const dim3 grid((unsigned)((b.max_count + per - 1) / per), (unsigned)b.n_seq);
+  const RowsArgs a = rows_args(g, layer, b, ld);
+  const dim3 grid = rows_grid(a);
   if (bf16) {
     const auto *kk = (const __nv_bfloat16*)k, *vv = (const __nv_bfloat16*)v;
-    return g.d == 64 ? launch(append_kernel<__nv_bfloat16, 64>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per)
-                     : launch(append_kernel<__nv_bfloat16, 128>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per);
+    return g.d == 64 ? launch(append_kernel<__nv_bfloat16, 64>, grid, 256, 0, st, false, a, kk, vv)
+                     : launch(append_kernel<__nv_bfloat16, 128>, grid, 256, 0, st, false, a, kk, vv);
   }
   const auto *kk = (const float*)k, *vv = (const float*)v;
-  return g.d == 64 ? launch(append_kernel<float, 64>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per)
-                   : launch(append_kernel<float, 128>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per);
+  return g.d == 64 ? launch(append_kernel<float, 64>, grid, 256, 0, st, false, a, kk, vv)
+                   : launch(append_kernel<float, 128>, grid, 256, 0, st, false, a, kk, vv);
 }
 
 cudaError_t kv4_read(const Kv4Geom& g, int layer, const Kv4Batch& b, void* k, void* v, long long ld, int bf16, cudaStream_t st) {
-  const int per = tokens_per_cta(g);
-  const dim3 grid((unsigned)((b.max_count + per - 1) / per), (unsigned)b.n_seq);
+  const RowsArgs a = rows_args(g, layer, b, ld);
+  const dim3 grid = rows_grid(a);
   if (bf16) {
     auto *kk = (__nv_bfloat16*)k, *vv = (__nv_bfloat16*)v;
-    return g.d == 64 ? launch(read_kernel<__nv_bfloat16, 64>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per)
-                     : launch(read_kernel<__nv_bfloat16, 128>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per);
+    return g.d == 64 ? launch(read_kernel<__nv_bfloat16, 64>, grid, 256, 0, st, false, a, kk, vv)
+                     : launch(read_kernel<__nv_bfloat16, 128>, grid, 256, 0, st, false, a, kk, vv);
   }
   auto *kk = (float*)k, *vv = (float*)v;
-  return g.d == 64 ? launch(read_kernel<float, 64>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per)
-                   : launch(read_kernel<float, 128>, grid, 256, 0, st, false, g, layer, b, kk, vv, ld, per);
+  return g.d == 64 ? launch(read_kernel<float, 64>, grid, 256, 0, st, false, a, kk, vv)
+                   : launch(read_kernel<float, 128>, grid, 256, 0, st, false, a, kk, vv);
 }
+
+namespace {
+template <int D, int NT>
+cudaError_t run_evict(const EvictArgs& a, size_t segs, cudaStream_t st) {
+  static std::atomic<bool> once[64];
+  const size_t words = (size_t)(a.max_rows + 31) / 32;
+  const size_t smem = (2 * words + 1) * 4 + (a.max_rows <= kKeysInSmem ? (size_t)a.max_rows * 4 : 0);
+  if (cudaError_t e = allow_smem((const void*)select_kernel<D, NT>, once, kSelectSmem)) return e;
+  if (cudaError_t e = launch(select_kernel<D, NT>, dim3((unsigned)segs), NT, smem, st, false, a)) return e;
+  return launch(move_kernel<D>, dim3((unsigned)((std::min(a.keep, a.max_rows) + kMove - 1) / kMove * segs)), 256, 0, st, true, a);
+}
+}  // namespace
 
 cudaError_t kv4_evict(const Kv4Geom& g, int layer0, int n_layers, int n_seq, int max_rows, const int32_t* rows,
                       const int32_t* tables, const int32_t* next_pos, int keep, int recent, const int32_t* out_tables,
                       int out_pages, int32_t* rows_out, int32_t* status, void* ws, cudaStream_t st) {
-  static std::atomic<bool> once[2][64];
   const size_t segs = (size_t)n_layers * n_seq * g.nkv;
   EvictArgs a;
   a.g = g;
@@ -381,15 +513,9 @@ cudaError_t kv4_evict(const Kv4Geom& g, int layer0, int n_layers, int n_seq, int
   a.map = reinterpret_cast<int32_t*>(w);
   a.movers = reinterpret_cast<int32_t*>(w + round256(segs * keep * 4));
   a.kept = reinterpret_cast<int32_t*>(w + 2 * round256(segs * keep * 4));
-  const size_t smem = (size_t)(max_rows + 31) / 32 * 4 + (max_rows <= kKeysInSmem ? (size_t)max_rows * 4 : 0);
-  if (cudaError_t e = allow_smem(g.d == 64 ? (const void*)select_kernel<64> : (const void*)select_kernel<128>, once[g.d == 128], kSelectSmem)) return e;
-  const dim3 mg((unsigned)((std::min(keep, max_rows) + kRows - 1) / kRows * segs));
-  if (g.d == 64) {
-    if (cudaError_t e = launch(select_kernel<64>, dim3((unsigned)segs), kSelThreads, smem, st, false, a)) return e;
-    return launch(move_kernel<64>, mg, 256, 0, st, false, a);
-  }
-  if (cudaError_t e = launch(select_kernel<128>, dim3((unsigned)segs), kSelThreads, smem, st, false, a)) return e;
-  return launch(move_kernel<128>, mg, 256, 0, st, false, a);
+  const bool few = max_rows <= 2048;  // (measured at 300 rows: 256 threads against 1,024)
+  if (g.d == 64) return few ? run_evict<64, 256>(a, segs, st) : run_evict<64, 1024>(a, segs, st);
+  return few ? run_evict<128, 256>(a, segs, st) : run_evict<128, 1024>(a, segs, st);
 }
 
 int kv4_config_check(const mbk_kv4_config* c) {

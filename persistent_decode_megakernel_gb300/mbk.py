@@ -66,7 +66,7 @@ class MbkWeights(ctypes.Structure):
 
 MBK_KV4_FP32, MBK_KV4_BF16 = 0, 1
 MBK_KV4_BAD_PAGE, MBK_KV4_BAD_BATCH, MBK_KV4_TIMEOUT = 1, 2, 4
-MBK_KV4_MAX_SEQS, MBK_KV4_MAX_EVICT_ROWS = 512, 1 << 20
+MBK_KV4_MAX_SEQS, MBK_KV4_MAX_EVICT_ROWS = 512, 1 << 19
 
 
 class MbkKv4Config(ctypes.Structure):
