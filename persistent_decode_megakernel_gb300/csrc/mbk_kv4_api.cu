@@ -118,7 +118,7 @@ int mbk_kv4_attention(const mbk_kv4_config* cfg, void* pool, int32_t layer, cons
     return MBK_ERR_INVALID_ARG;
   // the split counts blocks of rows in 32 bits, tiles of 8 query rows at least
   const double tiles = std::ceil((double)batch->max_count * (cfg->n_heads / cfg->n_kv_heads) / 8.0);
-  if (tiles * batch->n_seq * cfg->n_kv_heads * (batch->max_rows / 32 + 1) > 2e9) return MBK_ERR_INVALID_ARG;
+  if (tiles * batch->n_seq * cfg->n_kv_heads * (batch->max_rows / 32 + 1) > 2e9 || tiles > (1 << 24)) return MBK_ERR_INVALID_ARG;
   const int sms = sms_of(cfg->device);
   if (sms == 0) return MBK_ERR_UNSUPPORTED;
   const Kv4Geom g = kv4_geom(*cfg, pool);

@@ -65,6 +65,7 @@ struct AttnArgs {
   Kv4Batch b;
   Kv4Attn a;
   int layer, grp, grid_max, warps;
+  ByGroup by_grp;
   int below;     // query rows per KV head from which on a sequence is the prompt kernel's, or 0
   float scale2, cap_in, cap_out;  // scale log2(e); 2 / cap, cap log2(e)
   float* part;   // [grid][2][tile columns][d + 4] partial (o, m, l) of segments that several CTAs share
@@ -102,6 +103,29 @@ __device__ Split<TILE> make_split(const AttnArgs& a, SeqInfo* info, int* warp_su
   sp.track = a.g.track;
   sp.seq = info;
   int carry = 0;
+  if (a.b.n_seq <= 32) {
+    // every warp for itself, without a barrier; all write the same
+    const int s = threadIdx.x & 31;
+    SeqInfo q{0, 0, 0, 0};
+    int n = 0;
+    if (s < a.b.n_seq) {
+      const SeqView v = seq_view(a.g, a.b, s, report && threadIdx.x < 32);
+      q.r = v.r;
+      q.c = a.below == 0 || v.c * a.grp < a.below ? v.c : 0;  // longer ones are the prompt kernel's
+      q.tok0 = v.tok0;
+      n = sp.units(q);
+    }
+    int x = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, m);
+      if (s >= m) x += y;
+    }
+    q.cum = x - n;
+    if (s < a.b.n_seq) info[s] = q;
+    carry = __shfl_sync(0xffffffffu, x, 31);
+    __syncwarp();
+  } else {
   for (int s0 = 0; s0 < a.b.n_seq; s0 += blockDim.x) {
     const int s = s0 + threadIdx.x;
     SeqInfo q{0, 0, 0, 0};
@@ -119,6 +143,7 @@ __device__ Split<TILE> make_split(const AttnArgs& a, SeqInfo* info, int* warp_su
     carry += total;
   }
   __syncthreads();
+  }
   sp.total = carry;
   // one block for each warp of a CTA before a second CTA is used
   sp.grid = max(1, min(a.grid_max, (carry + a.warps - 1) / a.warps));
@@ -213,7 +238,7 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
   for (int ns = 0; ns < NS; ++ns) {
     // this lane: column gid, dims 16 tig .. + 15 of each group
     const int col = MODE == FP32_4 ? gid & 3 : 8 * ns + gid;
-    const int row = tile * P::TILE + col, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
+    const int row = tile * P::TILE + col, tok = row / a.by_grp, head = h * a.grp + row - tok * a.grp;
     const bool on = tok < sq.c;
     float x[kGroups][16], sum[kGroups];
     float mx = 0.f;
@@ -285,7 +310,7 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
           t.mid[g][j] = MODE == FP32_4 && tig >= 2 ? 0.f : m;  // the lo columns start at zero
         }
       }
-      const int crow = tile * P::TILE + column<MODE>(tig, ns, j), ctok = crow / a.grp;
+      const int crow = tile * P::TILE + column<MODE>(tig, ns, j), ctok = crow / a.by_grp;
       const bool con = ctok < sq.c;
       t.limit[ns][j] = con ? sq.r - sq.c + ctok : -1;
       if (FEAT > 0) {
@@ -594,7 +619,7 @@ __device__ __forceinline__ void finish(Acc<D, MODE>& A, const AttnArgs& a, const
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float l = all_rows(A.l[ns][j]);
-      const int col = column<MODE>(tig, ns, j), row = tile * P::TILE + col, tok = row / a.grp, head = h * a.grp + row - tok * a.grp;
+      const int col = column<MODE>(tig, ns, j), row = tile * P::TILE + col, tok = row / a.by_grp, head = h * a.grp + row - tok * a.grp;
       const bool on = tok < sq.c && !(MODE == FP32_4 && tig >= 2);
       const float inv = dep != nullptr ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
 #pragma unroll
@@ -664,13 +689,22 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
     SeqInfo psq = info[ps.s], csq = psq;
     unsigned have = 0;        // bit i: stage i holds a block to be used
     auto last_row = [&](const Seg& g, const SeqInfo& q) {  // last row that any query of the tile sees
-      const int tok = min(q.c - 1, (g.tile * TILE + TILE - 1) / a.grp);
+      const int tok = min(q.c - 1, (g.tile * TILE + TILE - 1) / a.by_grp);
       return q.r - q.c + tok;
     };
     int plast = last_row(ps, psq);
     const int32_t* table = a.b.tables + (size_t)ps.s * a.g.max_pages;
     const int page_mask = (1 << a.g.page_shift) / kRows - 1;
     auto page_of = [&](int blk) { return blk * kRows <= plast ? table[blk * kRows >> a.g.page_shift] : 0; };
+    {  // the first queries are asked for before the page numbers are waited for
+      const int row = cs.tile * TILE + (lane >> 2) % TILE, tok = row / a.by_grp;
+      if (tok < csq.c) {
+        const size_t at = (size_t)(csq.tok0 + tok) * a.a.ldq + (size_t)(cs.h * a.grp + row - tok * a.grp) * D;
+        constexpr int kBytes = P::kPrecise ? 4 : 2;
+        const unsigned char* p = reinterpret_cast<const unsigned char*>(a.a.q) + at * kBytes + (lane & 3) * (D * kBytes / 4);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+      }
+    }
     int page = page_of(ps.first + u0 - ps.u0);  // of the next block to be copied, asked for one block ahead
     auto issue = [&](int u) {
       if (u < u1) {
@@ -709,7 +743,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
       }
       load_q<D, MODE, FEAT>(qt, a, csq, cs.s, cs.h, cs.tile, lane);
       acc.clear();
-      const int first_limit = csq.r - csq.c + (cs.tile * TILE) / a.grp;
+      const int first_limit = csq.r - csq.c + (cs.tile * TILE) / a.by_grp;
       const int end = min(u1, cs.u0 + cs.n);
       for (; u < end; ++u) {
         const int stg = (u - u0) % kStages, blk = cs.first + u - cs.u0;
@@ -735,22 +769,32 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
     }
   }
   __syncthreads();
-  // join the warps' partials, segment by segment.  They lie in the order of the warps, and those of a segment
-  // are its first warp's last one (slot 1, unless it began before this CTA) and then first ones (slot 0).
-  for (int i = 0; i < 2 * kWarps;) {
-    const int seg = dep_seg[i >> 1][i & 1];
-    if (seg < 0) {
-      ++i;
-      continue;
+  // Join the warps' partials, a warp for each column of each segment.  They lie in the order of the warps, and those of a
+  // segment are its first warp's last one (slot 1, unless it began before this CTA) and then first ones (slot 0).
+  // Lane e looks at entry e = 2 warp + slot.
+  int seg = -1, ahead0 = -1, ahead1 = -1;
+  if (lane < 2 * kWarps) {
+    seg = dep_seg[lane >> 1][lane & 1];
+    if (lane >= 2) {
+      ahead0 = dep_seg[(lane >> 1) - 1][0];
+      ahead1 = dep_seg[(lane >> 1) - 1][1];
     }
-    int n = 1;
-    while ((i >> 1) + n < kWarps && dep_seg[(i >> 1) + n][0] == seg) ++n;
-    const Seg g = locate(sp, seg);
+  }
+  unsigned starts = __ballot_sync(0xffffffffu, seg >= 0 && ((lane & 1) || (seg != ahead0 && seg != ahead1)));
+  const int cols_max = dep_floats / P::kPart;
+  int turn = 0;
+  for (; starts != 0u; starts &= starts - 1) {
+    const int e = __ffs(starts) - 1, mine_seg = __shfl_sync(0xffffffffu, seg, e);
+    const unsigned more = __ballot_sync(0xffffffffu, seg == mine_seg && !(lane & 1) && lane > e);
+    const int n = 1 + __popc(more);
+    int col = (warp - turn) & (kWarps - 1);  // this warp's column of the segment, if it has one
+    turn += cols_max;
+    if (col >= cols_max) continue;
+    const Seg g = locate(sp, mine_seg);
     const SeqInfo sq = info[g.s];
     float* to = g.u0 >= c0 && g.u0 + g.n <= c1 ? nullptr : a.part + ((size_t)blockIdx.x * 2 + (g.u0 < c0 ? 0 : 1)) * TILE * P::kPart;
-    join<D>(a, sq, g.h, g.tile * TILE, min(TILE, sq.c * a.grp - g.tile * TILE), n, to,
-            [&](int k) { return k == 0 ? dep_at(i) : dep_at(2 * ((i >> 1) + k)); });
-    i = n == 1 ? i + 1 : 2 * ((i >> 1) + n - 1) + 1;
+    for (; col < min(TILE, sq.c * a.grp - g.tile * TILE); col += kWarps)
+      join_column<D>(a, sq, g.h, g.tile * TILE, col, n, to, [&](int k) { return k == 0 ? dep_at(e) : dep_at(2 * ((e >> 1) + k)); });
   }
 }
 
@@ -825,7 +869,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) weight_kernel(const __grid_
     if (p != nullptr && tig == 0) *reinterpret_cast<float4*>(old) = *reinterpret_cast<const float4*>(at);
     const unsigned char* st = mine + ((u - u0) & 1) * S::kBytes;
     for (int tile = 0; tile < tiles; ++tile) {
-      const int last = sq.r - sq.c + min(sq.c - 1, (tile * TILE + TILE - 1) / a.grp), first = sq.r - sq.c + tile * TILE / a.grp;
+      const int last = sq.r - sq.c + min(sq.c - 1, (tile * TILE + TILE - 1) / a.by_grp), first = sq.r - sq.c + (tile * TILE) / a.by_grp;
       if (p == nullptr || blk * kRows > last) continue;
       if (fresh || tiles > 1) {
         load_q<D, MODE, FEAT>(qt, a, sq, cs.s, cs.h, tile, lane);
@@ -833,7 +877,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) weight_kernel(const __grid_
         for (int ns = 0; ns < P::NS; ++ns)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int row = tile * TILE + column<MODE>(tig, ns, j), tok = row / a.grp, head = cs.h * a.grp + row - tok * a.grp;
+            const int row = tile * TILE + column<MODE>(tig, ns, j), tok = row / a.by_grp, head = cs.h * a.grp + row - tok * a.grp;
             // columns that hold no query, and the lo halves, add nothing
             lse[ns][j] = tok < sq.c && !(MODE == FP32_4 && tig >= 2) ? a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] : INFINITY;
           }
@@ -943,6 +987,7 @@ cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const 
   a.a = at;
   a.layer = layer;
   a.grp = g.nq / g.nkv;
+  a.by_grp = ByGroup::of(a.grp);
   a.grid_max = num_sms;
   a.scale2 = at.scale * kLog2e;
   a.cap_in = at.cap > 0.f ? 2.f / at.cap : 0.f;

@@ -670,15 +670,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const Item it = item_at(work, i);
       const SeqInfo sq = info[it.s];
       if (it.k0 >= it.k1 && (it.parts > 0 || it.split > 0)) continue;
-      const int qrow0 = it.tile * kItem + h * kQ, qrow = qrow0 + row, tok = qrow / a.grp, head = it.h * a.grp + qrow - tok * a.grp;
+      const int qrow0 = it.tile * kItem + h * kQ, qrow = qrow0 + row, tok = qrow / a.by_grp, head = it.h * a.grp + qrow - tok * a.grp;
       const bool on = tok < sq.c;
       auto qpos_of = [&](int token) { return (FEAT && a.b.positions != nullptr ? a.b.positions[it.s] : sq.r - sq.c) + token; };
       const int limit = on ? sq.r - sq.c + tok : -1;
-      const int first_limit = sq.r - sq.c + qrow0 / a.grp;
+      const int first_limit = sq.r - sq.c + qrow0 / a.by_grp;
       const bool whole_tile = qrow0 + kQ <= sq.c * a.grp;
       // first row inside the window of this query and of the tile's last, where positions are the rows' numbers
       const bool by_row = FEAT && a.a.window > 0 && !a.g.track;
-      const int low = by_row ? qpos_of(tok) - a.a.window + 1 : 0, last_low = by_row ? qpos_of(min(sq.c - 1, (qrow0 + kQ - 1) / a.grp)) - a.a.window + 1 : 0;
+      const int low = by_row ? qpos_of(tok) - a.a.window + 1 : 0, last_low = by_row ? qpos_of(min(sq.c - 1, (qrow0 + kQ - 1) / a.by_grp)) - a.a.window + 1 : 0;
       const int qpos = FEAT && on ? qpos_of(tok) : 0;
       const float slope = FEAT && on && a.a.slopes != nullptr ? a.a.slopes[head] * kLog2e : 0.f;
       // the row of q to the operand, its largest element scaled to [2^13, 2^14)
@@ -1016,6 +1016,7 @@ cudaError_t kv4_prompt(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4
   a.a = at;
   a.layer = layer;
   a.grp = g.nq / g.nkv;
+  a.by_grp = ByGroup::of(a.grp);
   a.least = least;
   a.slots = num_sms;
   a.scale2 = at.scale * kLog2e;
