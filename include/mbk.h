@@ -392,7 +392,7 @@ int mbk_kv4_read(const mbk_kv4_config *cfg, const void *pool, int32_t layer, con
  * the KV head's query heads.
  * Numerics: fp32 throughout for fp32 (operands of the tensor cores as fp16 pairs of 22 bits); for bf16 the
  * softmax weights are rounded to fp16.  Results do not depend on anything but the inputs and the GPU (no atomics).
- * workspace: mbk_kv4_attention_workspace(cfg, batch) bytes, 16-byte aligned, contents arbitrary. */
+ * workspace: mbk_kv4_attention_workspace(cfg, batch) bytes (0 is possible), 16-byte aligned, contents arbitrary. */
 int64_t mbk_kv4_attention_workspace(const mbk_kv4_config *cfg, const mbk_kv4_batch *batch);
 int mbk_kv4_attention(const mbk_kv4_config *cfg, void *pool, int32_t layer, const mbk_kv4_batch *batch, const void *q,
                       int64_t ldq, void *out, int64_t ldo, int32_t dtype, float scale, float cap, const float *slopes,

@@ -123,7 +123,8 @@ int mbk_kv4_attention(const mbk_kv4_config* cfg, void* pool, int32_t layer, cons
   if (sms == 0) return MBK_ERR_UNSUPPORTED;
   const Kv4Geom g = kv4_geom(*cfg, pool);
   const Kv4Batch b = batch_of(*batch);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < (int64_t)kv4_attention_workspace(g, b, sms)) return MBK_ERR_INVALID_ARG;
+  const int64_t need = (int64_t)kv4_attention_workspace(g, b, sms);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return MBK_ERR_INVALID_ARG;
   DeviceScope d(cfg->device);
   if (!d.ok) return MBK_ERR_CUDA;
   const Kv4Attn a{q, out, ldq, ldo, dtype == MBK_KV4_BF16, scale, cap, slopes, window, accumulate};

@@ -190,20 +190,31 @@ struct Stage {
   static constexpr int kBytes = 2 * kV + 128;
 };
 
+// A lane's places in a stage: where its first 16-byte chunk of codes goes (the later ones differ from it in bits 5
+// and 6 only), and where it reads K's rows 4 gid .., V's rows 8 tig .. and 8 tig + 4 ...
+struct LaneAt {
+  uint32_t put;
+  int k, v0, v1;
+};
+template <int D>
+__device__ __forceinline__ LaneAt lane_at(int lane) {
+  constexpr int kGroups = D / 64;
+  const int gid = lane >> 2, tig = lane & 3, r = lane / (2 * kGroups), in = lane % (2 * kGroups);
+  return LaneAt{(uint32_t)((in >> 1) * 1024 + place(r) + (in & 1) * 16), place(4 * gid) + 8 * tig, place(8 * tig) + 4 * gid, place(8 * tig + 4) + 4 * gid};
+}
+
 // Copies a block to a stage: K (PARTS 1) or K and V (2), and the positions.
 template <int D, int PARTS>
-__device__ __forceinline__ void fetch(uint32_t st, const uint8_t* blk, bool pos, int lane) {
+__device__ __forceinline__ void fetch(uint32_t st, const uint8_t* blk, bool pos, int lane, const LaneAt& at) {
   using S = Stage<D>;
   constexpr int kGroups = S::kGroups;
+  const uint8_t* src = blk + lane * 16;
+  const uint32_t put = st + at.put;  // stages begin at multiples of 128 bytes
 #pragma unroll
-  for (int sel = 0; sel < PARTS; ++sel) {
-    const uint8_t* src = blk + sel * half_bytes(D);
+  for (int sel = 0; sel < PARTS; ++sel)
 #pragma unroll
-    for (int i = 0; i < 2 * kGroups; ++i) {
-      const int c = i * 32 + lane, r = c / (2 * kGroups), in = c % (2 * kGroups);
-      cp16(st + sel * S::kV + (in >> 1) * 1024 + place(r) + (in & 1) * 16, src + c * 16);
-    }
-  }
+    for (int i = 0; i < 2 * kGroups; ++i)  // chunk 32 i + lane: a row 16 / kGroups further each time
+      cp16((put ^ (uint32_t)(i * (64 / kGroups))) + sel * S::kV, src + sel * half_bytes(D) + i * 512);
   // the pairs, 8 chunks a group, then the positions
   if (lane < PARTS * 8 * kGroups) {
     const int sel = lane / (8 * kGroups), c = lane % (8 * kGroups);
@@ -326,13 +337,13 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
 // full: every row of the block is visible to every query of the tile (a window aside).
 template <int D, int MODE, int FEAT>
 __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& a, const unsigned char* st, int blk, bool full, int lane,
-                                       float (&sc)[Shape<D, MODE>::NS][4][2]) {
+                                       const LaneAt& at, float (&sc)[Shape<D, MODE>::NS][4][2]) {
   using S = Stage<D>;
   using P = Shape<D, MODE>;
   constexpr int kGroups = P::kGroups, NS = P::NS, NT = P::NT;
   const int gid = lane >> 2, tig = lane & 3;
   // row 4 gid + i lies at place(4 gid) + 128 i
-  const unsigned char* kb = st + place(4 * gid) + 8 * tig;
+  const unsigned char* kb = st + at.k;
   uint32_t pr[kGroups * 4];
 #pragma unroll
   for (int i = 0; i < kGroups; ++i)
@@ -449,7 +460,7 @@ struct Acc {
 };
 
 template <int D, int MODE, int FEAT>
-__device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char* st, int blk, int rows, int lane,
+__device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char* st, int blk, int rows, int lane, const LaneAt& at,
                                            float (&sc)[Shape<D, MODE>::NS][4][2]) {
   using S = Stage<D>;
   using P = Shape<D, MODE>;
@@ -519,7 +530,7 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
       }
     }
   const float f = pow2i(kUnit - A.e);
-  const unsigned char *v0 = st + S::kV + place(8 * tig) + 4 * gid, *v1 = st + S::kV + place(8 * tig + 4) + 4 * gid;
+  const unsigned char *v0 = st + S::kV + at.v0, *v1 = st + S::kV + at.v1;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     uint32_t bf[NT][4];  // P^T as B fragments: register i holds rows 8 tig + i and 8 tig + 4 + i of column gid
@@ -699,13 +710,16 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
     {  // the first queries are asked for before the page numbers are waited for
       const int row = cs.tile * TILE + (lane >> 2) % TILE, tok = row / a.by_grp;
       if (tok < csq.c) {
-        const size_t at = (size_t)(csq.tok0 + tok) * a.a.ldq + (size_t)(cs.h * a.grp + row - tok * a.grp) * D;
+        const size_t from = (size_t)(csq.tok0 + tok) * a.a.ldq + (size_t)(cs.h * a.grp + row - tok * a.grp) * D;
         constexpr int kBytes = P::kPrecise ? 4 : 2;
-        const unsigned char* p = reinterpret_cast<const unsigned char*>(a.a.q) + at * kBytes + (lane & 3) * (D * kBytes / 4);
+        const unsigned char* p = reinterpret_cast<const unsigned char*>(a.a.q) + from * kBytes + (lane & 3) * (D * kBytes / 4);
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
       }
     }
     int page = page_of(ps.first + u0 - ps.u0);  // of the next block to be copied, asked for one block ahead
+    const LaneAt at = lane_at<D>(lane);
+    const uint8_t* src = nullptr;  // the block copied last
+    bool fresh = true;
     auto issue = [&](int u) {
       if (u < u1) {
         if (u >= ps.u0 + ps.n) {
@@ -714,19 +728,27 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
           plast = last_row(ps, psq);
           table = a.b.tables + (size_t)ps.s * a.g.max_pages;
           page = page_of(ps.first);
+          fresh = true;
         }
         const int blk = ps.first + u - ps.u0, stg = (u - u0) % kStages;
         have &= ~(1u << stg);
         if (blk * kRows <= plast) {
-          if ((unsigned)page < (unsigned)a.g.num_pages) {
-            have |= 1u << stg;
-            const uint8_t* p = a.g.pool + (size_t)page * a.g.page_stride + (size_t)(a.layer * a.g.nkv + ps.h) * a.g.head_stride +
-                               (unsigned)((blk & page_mask) * a.g.block_bytes);
-            fetch<D, 2>(mine_s + stg * S::kBytes, p, need_pos, lane);
-          } else if (lane == 0) {
-            flag(a.b.status, MBK_KV4_BAD_PAGE);
+          if (fresh) {  // the first block of a page, or of the run
+            src = nullptr;
+            if ((unsigned)page < (unsigned)a.g.num_pages)
+              src = a.g.pool + (size_t)page * a.g.page_stride + (size_t)(a.layer * a.g.nkv + ps.h) * a.g.head_stride +
+                    (unsigned)((blk & page_mask) * a.g.block_bytes);
+            else if (lane == 0)
+              flag(a.b.status, MBK_KV4_BAD_PAGE);
+          } else if (src != nullptr) {
+            src += a.g.block_bytes;
           }
-          if (((blk + 1) & page_mask) == 0) page = page_of(blk + 1);
+          if (src != nullptr) {
+            have |= 1u << stg;
+            fetch<D, 2>(mine_s + stg * S::kBytes, src, need_pos, lane, at);
+          }
+          fresh = ((blk + 1) & page_mask) == 0;
+          if (fresh) page = page_of(blk + 1);
         }
       }
       cp_commit();
@@ -754,8 +776,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::kWarps * 32) attn_kernel(const
         if (use) {
           const unsigned char* st = mine + stg * S::kBytes;
           float sc[P::NS][4][2];
-          scores<D, MODE, FEAT>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first_limit, lane, sc);
-          accumulate<D, MODE, FEAT>(acc, st, blk, csq.r, lane, sc);
+          scores<D, MODE, FEAT>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first_limit, lane, at, sc);
+          accumulate<D, MODE, FEAT>(acc, st, blk, csq.r, lane, at, sc);
         }
         __syncwarp();
       }
@@ -839,6 +861,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) weight_kernel(const __grid_
   const int u0 = c0 + warp * wb + min(warp, we), u1 = u0 + wb + (warp < we ? 1 : 0);
   if (u0 >= u1) return;
   Seg ps = locate(sp, u0);
+  const LaneAt here = lane_at<D>(lane);
   uint8_t* next = nullptr;  // the block that is being copied
   auto issue = [&](int u) {
     next = nullptr;
@@ -846,7 +869,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) weight_kernel(const __grid_
       if (u >= ps.u0 + ps.n) ps = locate(sp, u);
       const int blk = ps.first + u - ps.u0;
       if (blk * kRows < info[ps.s].r) next = block_of(a.g, a.b.tables + (size_t)ps.s * a.g.max_pages, a.layer, ps.h, blk * kRows, nullptr);
-      if (next != nullptr) fetch<D, 1>(smem_of(mine) + ((u - u0) & 1) * S::kBytes, next, FEAT > 0, lane);
+      if (next != nullptr) fetch<D, 1>(smem_of(mine) + ((u - u0) & 1) * S::kBytes, next, FEAT > 0, lane, here);
     }
     cp_commit();
   };
@@ -886,7 +909,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) weight_kernel(const __grid_
       cp_wait<1>();
       __syncwarp();
       float sc[P::NS][4][2];
-      scores<D, MODE, FEAT>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first, lane, sc);
+      scores<D, MODE, FEAT>(qt, a, st, blk, (blk + 1) * kRows - 1 <= first, lane, here, sc);
 #pragma unroll
       for (int ns = 0; ns < P::NS; ++ns)
 #pragma unroll
@@ -970,7 +993,8 @@ bool has_prompts(const Kv4Geom& g, const Kv4Batch& b, int bf16) {
   return (long long)b.max_count * (g.nq / g.nkv) >= kPromptRows && (bf16 || g.d == 64);
 }
 size_t part_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
-  const size_t own = round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
+  // none where one CTA's warps have a block each, whatever the queries' type (tiles of 4 at least)
+  const size_t own = max_units(g, b, 4) <= (g.d == 64 ? 16 : 8) ? 0 : round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
   return own + ((long long)b.max_count * (g.nq / g.nkv) >= kPromptRows ? round256(kv4_prompt_partials(g, b, num_sms)) : 0);
 }
 
@@ -999,7 +1023,7 @@ cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const 
   if (prompts) {
     // a sequence alone goes to the prompt kernel however few its tokens turn out to be
     a.below = b.n_seq == 1 ? 1 : kPromptRows;
-    uint8_t* part = reinterpret_cast<uint8_t*>(ws) + round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
+    uint8_t* part = reinterpret_cast<uint8_t*>(ws) + round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);  // (a prompt has many units)
     if (cudaError_t e = kv4_prompt(g, layer, b, at, a.below, reinterpret_cast<float*>(part), a.lse, num_sms, st)) return e;
   }
   const bool others = !prompts || b.n_seq > 1;

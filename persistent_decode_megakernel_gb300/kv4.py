@@ -66,6 +66,7 @@ class Kv4Cache:
         if pool.dtype != torch.uint8 or not pool.is_contiguous() or pool.numel() != self.bytes or not pool.is_cuda:
             raise ValueError(f"pool: a contiguous uint8 CUDA tensor of {self.bytes} bytes")
         self.pool = pool
+        self._evict_bytes = {}  # the last eviction's workspace size, by its arguments
         self._pool = pool.data_ptr()
         # errors that only the kernels see (bits MBK_KV4_BAD_PAGE, MBK_KV4_BAD_BATCH), since the last clear
         self.status_word = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -77,8 +78,7 @@ class Kv4Cache:
         return int(n)
 
     def _ints(self, name: str, t, shape) -> None:
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous() or \
-                tuple(t.shape) != tuple(shape):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != self.device or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: a contiguous int32 tensor {tuple(shape)} on {self.device}")
 
     def _rows(self, name: str, t, n: int, heads: int):
@@ -160,11 +160,12 @@ class Kv4Cache:
         if slopes is not None and (slopes.dtype != torch.float32 or slopes.device != self.device or not slopes.is_contiguous() or
                                    slopes.shape != (cfg.n_heads,)):
             raise ValueError(f"slopes: a contiguous fp32 tensor {(cfg.n_heads,)} on {self.device}")
-        ws = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=self.device)
+        ws = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=self.device) if batch.workspace_bytes else None
         rc = self.lib.mbk_kv4_attention(self._cfg, self._pool, layer, batch.ref, qp, ldq, op, ldo, _DTYPES[q.dtype],
                                         cfg.head_dim ** -0.5 if scale is None else scale, cap, _ptr(slopes), window, int(accumulate),
-                                        ws.data_ptr(), batch.workspace_bytes, self._stream())
-        mbk._check(rc, "mbk_kv4_attention")
+                                        _ptr(ws), batch.workspace_bytes, _raw_stream(self.index))
+        if rc != mbk.MBK_OK:
+            raise mbk.MbkError(rc, "mbk_kv4_attention")
         return out
 
     def evict(self, rows, tables, next_pos, keep: int, recent: int = 0, out_tables=None, layer: int = 0, n_layers: Optional[int] = None,
@@ -182,10 +183,15 @@ class Kv4Cache:
             self._ints("out_tables", out_tables, (n_seq, out_pages))
         if rows_out is None:
             rows_out = torch.empty_like(rows)
-        self._ints("rows_out", rows_out, (n_seq,))
+        else:
+            self._ints("rows_out", rows_out, (n_seq,))
         n_layers = cfg.n_layers - layer if n_layers is None else n_layers
         max_rows = min(cfg.max_pages * cfg.page_size, mbk.MBK_KV4_MAX_EVICT_ROWS) if max_rows is None else max_rows
-        size = self._size(self.lib.mbk_kv4_evict_workspace(self._cfg, n_layers, n_seq, keep), "mbk_kv4_evict_workspace")
+        key = (n_layers, n_seq, keep)
+        size = self._evict_bytes.get(key)
+        if size is None:
+            size = self._size(self.lib.mbk_kv4_evict_workspace(self._cfg, n_layers, n_seq, keep), "mbk_kv4_evict_workspace")
+            self._evict_bytes = {key: size}
         ws = torch.empty(size, dtype=torch.uint8, device=self.device)
         rc = self.lib.mbk_kv4_evict(self._cfg, self._pool, layer, n_layers, n_seq, max_rows, _ptr(rows), _ptr(tables), _ptr(next_pos), keep,
                                     recent, _ptr(out_tables), out_pages, _ptr(rows_out), _ptr(self.status_word), ws.data_ptr(), size,
