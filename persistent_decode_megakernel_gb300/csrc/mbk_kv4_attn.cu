@@ -228,8 +228,8 @@ template <int D, int MODE>
 struct QTile {
   using P = Shape<D, MODE>;
   uint32_t f[P::kGroups][4][P::NT][2];
-  float mul[P::NS][2], add[P::kGroups][P::NS][2];  // score = scale_r * acc * mul + z_r * add, in the base-2 logarithm's units
-  float mid[P::kGroups][2];                        // fp32: -7.5 sum(q) in acc's units; codes count from their middle
+  float mul[P::NS][2], add[P::kGroups][P::NS][2];  // score = mul * sum of (scale_r * acc + z_r * add), in the base-2 logarithm's units
+  float mid[P::kGroups][2];                        // fp32: -7.5 add: codes count from their middle
   int limit[P::NS][2], qpos[P::NS][2];             // last visible row (-1: none), position
   float slope[P::NS][2];
 };
@@ -315,10 +315,9 @@ __device__ __forceinline__ void load_q(QTile<D, MODE>& t, const AttnArgs& a, con
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const float sg = __shfl_sync(0xffffffffu, sum[g], from);
-        t.add[g][ns][j] = sg * a.scale2;
+        t.add[g][ns][j] = sg * (1.f / 16777216.f) * __shfl_sync(0xffffffffu, up, from);  // sum(q) in acc's units
         if (P::kPrecise) {
-          const float m = sg * (-7.5f / 16777216.f) * __shfl_sync(0xffffffffu, up, from);
-          t.mid[g][j] = MODE == FP32_4 && tig >= 2 ? 0.f : m;  // the lo columns start at zero
+          t.mid[g][j] = MODE == FP32_4 && tig >= 2 ? 0.f : -7.5f * t.add[g][ns][j];  // the lo columns start at zero
         }
       }
       const int crow = tile * P::TILE + column<MODE>(tig, ns, j), ctok = crow / a.by_grp;
@@ -341,7 +340,7 @@ __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& 
   using S = Stage<D>;
   using P = Shape<D, MODE>;
   constexpr int kGroups = P::kGroups, NS = P::NS, NT = P::NT;
-  const int gid = lane >> 2, tig = lane & 3;
+  const int gid = lane >> 2;
   // row 4 gid + i lies at place(4 gid) + 128 i
   const unsigned char* kb = st + at.k;
   uint32_t pr[kGroups * 4];
@@ -383,9 +382,8 @@ __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& 
             float acc = c[ns][2 * i + j];
             if (MODE == FP32_8) acc += c[NT - 1][2 * i + j];
             if (MODE == FP32_4) acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-            const float x = fmaf(p.x, acc * t.mul[ns][j], z * t.add[g][ns][j]);
-            if (g == 0) sc[ns][2 * mt + i][j] = x;
-            else sc[ns][2 * mt + i][j] += x;
+            float& x = sc[ns][2 * mt + i][j];
+            x = fmaf(p.x, acc, g == 0 ? z * t.add[g][ns][j] : fmaf(z, t.add[g][ns][j], x));
           }
       }
     }
@@ -399,9 +397,13 @@ __device__ __forceinline__ void scores(const QTile<D, MODE>& t, const AttnArgs& 
       for (int j = 0; j < 2; ++j) {
         // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap))): off by a few 2^-24 of cap
         float& x = sc[i / 4][i % 4][j];
-        const float e = ex2(fminf(x * a.cap_in, 126.f));
-        x = fmaf(-a.cap_out, __fdividef(2.f, 1.f + e), a.cap_out);
+        x = fmaf(-2.f * a.cap_out, rcp(1.f + ex2(x * (t.mul[i / 4][j] * a.cap_in))), a.cap_out);
       }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * NS; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sc[i / 4][i % 4][j] *= t.mul[i / 4][j];
   }
   if (FEAT > 0 && (a.a.slopes != nullptr || (FEAT == 2 && a.a.window > 0))) {
     int kpos[4];
@@ -483,13 +485,14 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
 #pragma unroll
   for (int i = 1; i < 4 * kGroups; ++i) mx = __hmax2(mx, *reinterpret_cast<const __half2*>(&pr[i]));
   const int eb = min((int)((*reinterpret_cast<const uint32_t*>(&mx) >> 10) & 31u) - 15, 15);  // of the largest scale (low halves)
-  bool over = eb > A.e;
+  // how far the scores exceed their columns' reference (a reference of -inf: by -inf or inf; NaN does not count)
+  float over = -INFINITY;
 #pragma unroll
   for (int ns = 0; ns < NS; ++ns)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      over = over || fmaxf(fmaxf(sc[ns][0][j], sc[ns][1][j]), fmaxf(sc[ns][2][j], sc[ns][3][j])) > A.m[ns][j] + kSlack;
-  if (__any_sync(0xffffffffu, over)) {
+      over = fmaxf(over, fmaxf(fmaxf(sc[ns][0][j], sc[ns][1][j]), fmaxf(sc[ns][2][j], sc[ns][3][j])) - fmaxf(A.m[ns][j], -3e38f));
+  if (__any_sync(0xffffffffu, (over > kSlack) | (eb > A.e))) {
     const int e = max(A.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)(eb + 32)) - 32);
     const float unit = pow2i(A.e - e);
     A.e = e;
