@@ -6,10 +6,11 @@ namespace mbk {
 namespace {
 
 // ------------------------------------------------------------------ append and read
-// A row -- the K or V of one token and KV head -- is d / 8 lanes of 8 elements.  A CTA takes `per` tokens of one
-// sequence (grid.y), two rows per lane at a time.  Both are bound by the bytes once the instructions for an
-// element are few: no division by the number of heads (a multiplication by its reciprocal), codes through the low
-// bits of a large float or half instead of conversions (one in four clocks).
+// A row -- the K or V of one token and KV head -- is d / 16 lanes of 16 elements.  A CTA takes `per` tokens of one
+// sequence (grid.y).  Both are bound by instructions rather than bytes unless those for an element are few: 16
+// elements share a row's address, there is no division by the number of heads (a multiplication by its
+// reciprocal), codes go through the low bits of a large float or half instead of conversions (one in four
+// clocks), and arithmetic goes two values at a time.
 struct RowsArgs {
   Kv4Geom g;
   Kv4Batch b;
@@ -37,20 +38,38 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The codes of 8 elements: (x - lo) / scale to nearest even, in 0 .. 15.  The product with 1 / scale is within 2^-22
 // of the quotient's 15 at most, so only where one lies nearer than 1e-5 to a half the divisions themselves are made
-// (bf16 inputs do meet exact halves).  Adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low bits.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float lo, float scale, float inv) {
+// (bf16 inputs do meet exact halves).  Adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low bits; the
+// words add up with the big number's own bits, which are taken off at the end.
+__device__ __forceinline__ uint32_t codes_of(const float* x, float lo, float scale, float inv) {
   constexpr float kBig = 12582912.f;
-  float q[8], far = 0.f;
+  constexpr uint32_t kBits = 0x4b400000u, kExtra = kBits * 0x11111111u;  // kBits << 0, 4, .. 28 added up
+  const f2 less = pair_of(-lo, -lo), by = pair_of(inv, inv), big = pair_of(kBig, kBig), no_big = pair_of(-kBig, -kBig), minus = pair_of(-1.f, -1.f);
+  float far = 0.f;
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], lo), inv), 0.f), 15.f);
-    const float r = __fadd_rn(q[i], kBig);
-    far = fmaxf(far, fabsf(__fsub_rn(q[i], __fsub_rn(r, kBig))));
-    w |= (__float_as_uint(r) & 15u) << (4 * i);
+  for (int i = 0; i < 8; i += 2) {
+    float2 q = halves(mul2(sum2(pair_of(x[i], x[i + 1]), less), by));
+    q.x = fminf(fmaxf(q.x, 0.f), 15.f);
+    q.y = fminf(fmaxf(q.y, 0.f), 15.f);
+    const f2 c = pair_of(q.x, q.y), r = sum2(c, big);
+    const float2 d = halves(fma2(sum2(r, no_big), minus, c)), rr = halves(r);
+    far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+    w += __float_as_uint(rr.x) * (1u << (4 * i)) + __float_as_uint(rr.y) * (1u << (4 * i + 4));
   }
+  w -= kExtra;
   if (far > 0.49999f) {
     w = 0;
 #pragma unroll
@@ -61,7 +80,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float lo, floa
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ RowsArgs a, const T* k, const T* v) {
-  constexpr int V = D / 8, kStep = 256 / V;  // lanes of a row, rows of a step
+  constexpr int V = D / 16, kStep = 256 / V;  // lanes of a row, rows of a step
   const Kv4Geom& g = a.g;
   const int s = blockIdx.y, t0 = blockIdx.x * a.per;
   const SeqView q = seq_view(g, a.b, s, threadIdx.x == 0 && blockIdx.x == 0);
@@ -73,52 +92,53 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Row
   const int rows = min(a.per, q.c - t0) * g.nkv * 2, j = threadIdx.x % V, first = threadIdx.x / V;
   const int32_t* table = a.b.tables + (size_t)s * g.max_pages;
   const int p0 = a.b.positions != nullptr ? a.b.positions[s] : q.r - q.c;
-  for (int r0 = 0; r0 < rows; r0 += 2 * kStep) {  // all lanes of a warp go round together
-    RowAt at[2];
-    float x[2][8];
-    bool on[2];
+  for (int r0 = 0; r0 < rows; r0 += kStep) {  // all lanes of a warp go round together
+    const bool on = r0 + first < rows;
+    RowAt at = row_at(a, on ? r0 + first : 0);
+    at.t += t0;
+    const T* from = (at.sel ? v : k) + (size_t)(q.tok0 + at.t) * a.ld + at.h * D + 16 * j;
+    float x[16];
+    load8<T>(from, *reinterpret_cast<float(*)[8]>(&x[0]));
+    load8<T>(from + 8, *reinterpret_cast<float(*)[8]>(&x[8]));
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = r0 + u * kStep + first;
-      on[u] = r < rows;
-      at[u] = row_at(a, on[u] ? r : 0);
-      at[u].t += t0;
-      load8<T>((at[u].sel ? v : k) + (size_t)(q.tok0 + at[u].t) * a.ld + at[u].h * D + 8 * j, x[u]);
+    for (int i = 1; i < 15; i += 2) {
+      lo = min3_nan(lo, x[i], x[i + 1]);
+      hi = max3_nan(hi, x[i], x[i + 1]);
     }
+    lo = min_nan(lo, x[15]);
+    hi = max_nan(hi, x[15]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float lo = INFINITY, hi = -INFINITY;
+    for (int m = 1; m < 4; m <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+    }
+    if (!(lo >= -65504.f && hi <= 65504.f)) {  // beyond fp16, or NaN, which stays
+      lo = lo != lo ? lo : fminf(fmaxf(lo, -65504.f), 65504.f);
+      hi = hi != hi ? hi : fminf(fmaxf(hi, -65504.f), 65504.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo = min_nan(lo, x[u][i]);
-        hi = max_nan(hi, x[u][i]);
-      }
-#pragma unroll
-      for (int m = 1; m < 8; m <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-      }
-      if (!(lo >= -65504.f && hi <= 65504.f)) {  // beyond fp16, or NaN, which stays
-        lo = lo != lo ? lo : fminf(fmaxf(lo, -65504.f), 65504.f);
-        hi = hi != hi ? hi : fminf(fmaxf(hi, -65504.f), 65504.f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] = fminf(fmaxf(x[u][i], -65504.f), 65504.f);
-      }
-      const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), lh = __float2half_rn(lo);
-      const float sf = __half2float(sh), lf = __half2float(lh);
-      // a constant group, and one with a NaN, has codes of zero
-      const uint32_t w = sf > 0.f ? codes_of(x[u], lf, sf, __fdiv_rn(1.f, sf)) : 0u;
-      if (!on[u]) continue;
-      const int row = q.r - q.c + at[u].t, lane_row = row % kRows;
-      uint8_t* blk = block_of(g, table, a.layer, at[u].h, row, a.b.status);
-      if (blk == nullptr) continue;
-      uint8_t* base = blk + at[u].sel * half_bytes(D);
-      *reinterpret_cast<uint32_t*>(base + lane_row * (D / 2) + 4 * j) = w;
-      if (j % 8 == 0)
-        *reinterpret_cast<__half2*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 8) * 4) = __halves2half2(sh, lh);
-      if (g.track && at[u].sel == 0 && j == 0) {
-        *reinterpret_cast<int32_t*>(blk + pos_at(D) + 4 * lane_row) = p0 + at[u].t;
-        *reinterpret_cast<float*>(blk + weight_at(D) + 4 * lane_row) = 0.f;
+      for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
+    }
+    const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f)), lh = __float2half_rn(lo);
+    const float sf = __half2float(sh), lf = __half2float(lh);
+    uint2 w = make_uint2(0u, 0u);  // a constant group, and one with a NaN, has codes of zero
+    if (sf > 0.f) {
+      const float inv = __fdiv_rn(1.f, sf);
+      w.x = codes_of(x, lf, sf, inv);
+      w.y = codes_of(x + 8, lf, sf, inv);
+    }
+    if (on) {
+      const int row = q.r - q.c + at.t, lane_row = row % kRows;
+      uint8_t* blk = block_of(g, table, a.layer, at.h, row, a.b.status);
+      if (blk != nullptr) {
+        uint8_t* base = blk + at.sel * half_bytes(D);
+        *reinterpret_cast<uint2*>(base + lane_row * (D / 2) + 8 * j) = w;
+        if (j % 4 == 0)
+          *reinterpret_cast<__half2*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 4) * 4) = __halves2half2(sh, lh);
+        if (g.track && at.sel == 0 && j == 0) {
+          *reinterpret_cast<int32_t*>(blk + pos_at(D) + 4 * lane_row) = p0 + at.t;
+          *reinterpret_cast<float*>(blk + weight_at(D) + 4 * lane_row) = 0.f;
+        }
       }
     }
   }
@@ -126,7 +146,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Row
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ RowsArgs a, T* k, T* v) {
-  constexpr int V = D / 8, kStep = 256 / V, kAtOnce = 4;
+  constexpr int V = D / 16, kStep = 256 / V, kAtOnce = 2;
   const Kv4Geom& g = a.g;
   const int s = blockIdx.y, t0 = blockIdx.x * a.per;
   const SeqView q = seq_view(g, a.b, s, threadIdx.x == 0 && blockIdx.x == 0);
@@ -137,41 +157,50 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ RowsA
   }
   const int rows = min(a.per, q.c - t0) * g.nkv * 2, j = threadIdx.x % V, first = threadIdx.x / V;
   const int32_t* table = a.b.tables + (size_t)s * g.max_pages;
+  // a lane's 16 elements are 8 of each half of the row, so that neighbouring lanes write neighbouring bytes
   for (int r0 = 0; r0 < rows; r0 += kAtOnce * kStep) {
-    uint32_t w[kAtOnce], pr[kAtOnce];
-    size_t to[kAtOnce];
-    int sel[kAtOnce];
+    uint32_t w[kAtOnce][2], pr[kAtOnce][2];
+    T* to[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int r = r0 + u * kStep + first;
-      sel[u] = -1;
-      if (r >= rows) continue;
-      RowAt at = row_at(a, r);
-      at.t += t0;
-      const int row = q.r - q.c + at.t, lane_row = row % kRows;
-      const uint8_t* blk = block_of(g, table, a.layer, at.h, row, a.b.status);
-      const uint8_t* base = blk + at.sel * half_bytes(D);
-      sel[u] = at.sel;
-      to[u] = (size_t)(q.tok0 + at.t) * a.ld + at.h * D + 8 * j;
-      w[u] = pr[u] = 0u;  // a bad page reads as zero
-      if (blk != nullptr) {
-        w[u] = __ldg(reinterpret_cast<const uint32_t*>(base + lane_row * (D / 2) + 4 * j));
-        pr[u] = __ldg(reinterpret_cast<const uint32_t*>(base + code_bytes(D) + (lane_row * (D / 64) + j / 8) * 4));
+      to[u] = nullptr;
+      if (r < rows) {
+        RowAt at = row_at(a, r);
+        at.t += t0;
+        const int row = q.r - q.c + at.t, lane_row = row % kRows;
+        const uint8_t* blk = block_of(g, table, a.layer, at.h, row, a.b.status);
+        const uint8_t* base = blk + at.sel * half_bytes(D);
+        to[u] = (at.sel ? v : k) + (size_t)(q.tok0 + at.t) * a.ld + at.h * D + 8 * j;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          w[u][hf] = pr[u][hf] = 0u;  // a bad page reads as zero
+          if (blk != nullptr) {
+            w[u][hf] = __ldg(reinterpret_cast<const uint32_t*>(base + lane_row * (D / 2) + hf * (D / 4) + 4 * j));
+            pr[u][hf] = __ldg(reinterpret_cast<const uint32_t*>(base + code_bytes(D) + (lane_row * (D / 64) + hf * (D / 128)) * 4));
+          }
+        }
       }
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      if (sel[u] < 0) continue;
-      const float2 p = unpack_half(pr[u]);
-      float x[8];
+      if (to[u] == nullptr) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // codes i and i + 4 as 1024 + code in fp16
-        const uint32_t c = (w[u] >> (4 * i) & 0x000f000fu) | 0x64006400u;
-        const float2 f = __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1024.f)));
-        x[i] = fmaf(p.x, f.x, p.y);
-        x[i + 4] = fmaf(p.x, f.y, p.y);
+      for (int hf = 0; hf < 2; ++hf) {
+        const float2 p = unpack_half(pr[u][hf]);
+        const f2 scale = pair_of(p.x, p.x), lo = pair_of(p.y, p.y);
+        const uint32_t word = w[u][hf];
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // codes i and i + 4 as 1024 + code in fp16
+          const uint32_t c = (word >> (4 * i) & 0x000f000fu) | 0x64006400u;
+          const float2 f = __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1024.f)));
+          const float2 y = halves(fma2(pair_of(f.x, f.y), scale, lo));
+          x[i] = y.x;
+          x[i + 4] = y.y;
+        }
+        store8(to[u] + hf * (D / 2), x);
       }
-      store8((sel[u] ? v : k) + to[u], x);
     }
   }
 }
@@ -425,8 +454,8 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Evict
   }
 }
 
-// Tokens of a CTA of append and read: about 2,048 vectors of 8.
-int tokens_per_cta(const Kv4Geom& g) { return std::max(1, 2048 / (g.nkv * 2 * (g.d / 8))); }
+// Tokens of a CTA of append and read: about 1,024 vectors of 16.
+int tokens_per_cta(const Kv4Geom& g) { return std::max(1, 1024 / (g.nkv * 2 * (g.d / 16))); }
 
 constexpr int kSelectSmem = 208 * 1024;  // dynamic shared memory of the selection: 227 KB less its static part
 
