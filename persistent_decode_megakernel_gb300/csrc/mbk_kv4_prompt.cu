@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __shared__ unsigned failed;
   __shared__ TileNote notes[kNotes];
   __shared__ int sums[kThreads / 32];
+  __shared__ float2 row_scale[kItem];
   unsigned char* smem = raw_smem + ((1024u - (smem_of(raw_smem) & 1023u)) & 1023u);
   SeqInfo* info = reinterpret_cast<SeqInfo*>(smem + L::kInfoAt);
   const int warp = threadIdx.x >> 5;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------ softmax: one query row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    const int h = warp >> 2, row = threadIdx.x & 127;  // query tile, row
+    const int h = warp >> 2, row = threadIdx.x & 127, lane = threadIdx.x & 31, wrow0 = (warp & 3) * 32;  // query tile, row, the warp's first
     const uint32_t mine = tmem + h * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_out = mine + 2 * kKeys, t_sum = t_out + 64;  // this lane's columns
     bool ok = true;
     for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
@@ -648,63 +649,67 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int low = by_row ? qpos_of(tok) - a.a.window + 1 : 0, last_low = by_row ? qpos_of(min(sq.c - 1, (qrow0 + kQ - 1) / a.by_grp)) - a.a.window + 1 : 0;
       const int qpos = FEAT && on ? qpos_of(tok) : 0;
       const float slope = FEAT && on && a.a.slopes != nullptr ? a.a.slopes[head] * kLog2e : 0.f;
-      // the row of q to the operand, its largest element scaled to [2^13, 2^14)
-      float mul, addm = 0.f;  // score = mul * (acc, or fp32: scale_r acc + z_r addm)
+      // The warp's 32 rows of q to the operand, each row's largest element scaled to [2^13, 2^14): neighbouring lanes read
+      // a row's neighbouring 16 bytes (a row a thread would be 32 lines an instruction), all of them before the first is used.
+      constexpr int kLanes = D * (FP32 ? 4 : 2) / 16, kRowsAtOnce = 32 / kLanes, kLoads = 32 / kRowsAtOnce;
       {
-        float mx = 0.f, sum = 0.f;
-        const size_t at = (size_t)(sq.tok0 + (on ? tok : 0)) * a.a.ldq + (size_t)head * D;
-        // the whole row at once: 64 registers, one wait
-        constexpr int kVec = FP32 ? D / 4 : D / 8;
-        uint4 q[kVec];
-        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(a.a.q) + at * (FP32 ? 4 : 2));
+        uint4 q[kLoads];
+        const unsigned char* base = reinterpret_cast<const unsigned char*>(a.a.q);
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) q[c] = on ? __ldg(from + c) : make_uint4(0u, 0u, 0u, 0u);
-        auto get = [&](int c, float(&x)[8]) {
-          if (FP32) {
-            const uint4 u = q[(2 * c) % kVec], v = q[(2 * c + 1) % kVec];
-            x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
-            x[4] = __uint_as_float(v.x), x[5] = __uint_as_float(v.y), x[6] = __uint_as_float(v.z), x[7] = __uint_as_float(v.w);
+        for (int c = 0; c < kLoads; ++c) {
+          const int r = wrow0 + c * kRowsAtOnce + lane / kLanes, t = (qrow0 + r) / a.by_grp, hd = it.h * a.grp + qrow0 + r - t * a.grp;
+          q[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (t < sq.c)
+            q[c] = __ldg(reinterpret_cast<const uint4*>(base + ((size_t)(sq.tok0 + t) * a.a.ldq + (size_t)hd * D) * (FP32 ? 4 : 2)) + lane % kLanes);
+        }
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+          float x[8], mx = 0.f, sum = 0.f;
+          const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+          if (FP32) {  // four dims; the neighbour has the other four of the eight
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float mine = __uint_as_float(w[e]), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+              x[e] = (lane & 1) ? other : mine;
+              x[e + 4] = (lane & 1) ? mine : other;
+              mx = fmaxf(mx, fabsf(mine));
+              sum += mine;
+            }
           } else {
-            const uint32_t w[4] = {q[c % kVec].x, q[c % kVec].y, q[c % kVec].z, q[c % kVec].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               x[2 * e] = __uint_as_float(w[e] << 16);
               x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+              mx = fmaxf(mx, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
             }
           }
-        };
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          float x[8];
-          get(c, x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            mx = fmaxf(mx, fabsf(x[e]));
-            sum += x[e];
+          for (int i = 1; i < kLanes; i <<= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+            if (FP32) sum += __shfl_xor_sync(0xffffffffu, sum, i);
           }
-        }
-        int ex = (__float_as_int(mx) >> 23) & 255;
-        ex = ex == 255 ? 140 : max(ex, 20);
-        const float up = a.scale2 < 0.f ? -pow2i(140 - ex) : pow2i(140 - ex);  // mul >= 0: the largest acc is the largest score
-        mul = pow2i(ex - 140) * fabsf(a.scale2);
-        if (FP32) addm = sum * up;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          float x[8];
-          get(c, x);
-          uint32_t hi[4], lo[4];
+          int ex = (__float_as_int(mx) >> 23) & 255;
+          ex = ex == 255 ? 140 : max(ex, 20);
+          const float up = a.scale2 < 0.f ? -pow2i(140 - ex) : pow2i(140 - ex);  // mul >= 0: the largest acc is the largest score
+          const int r = wrow0 + c * kRowsAtOnce + lane / kLanes;
+          if (lane % kLanes == 0) row_scale[h * kQ + r] = make_float2(pow2i(ex - 140) * fabsf(a.scale2), sum * up);
+          uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // the conversion's order of dims: 0 4 1 5 2 6 3 7
             const float x0 = x[e] * up, x1 = x[e + 4] * up;
-            hi[e] = pack_half(x0, x1);
-            const float2 u = unpack_half(hi[e]);
-            lo[e] = pack_half(x0 - u.x, x1 - u.y);
+            o[e] = pack_half(x0, x1);
+            if (FP32 && (lane & 1)) {  // even lanes write hi, odd ones lo
+              const float2 u = unpack_half(o[e]);
+              o[e] = pack_half(x0 - u.x, x1 - u.y);
+            }
           }
-          unsigned char* to = smem + L::kQAt + h * L::kQTile + (c >> 3) * kQ * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (FP32) *reinterpret_cast<uint4*>(to + kGroups * kQ * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          const int chunk = FP32 ? (lane % kLanes) / 2 : lane % kLanes;
+          unsigned char* to = smem + L::kQAt + h * L::kQTile + (chunk >> 3) * kQ * 128 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(to + (FP32 && (lane & 1) ? kGroups * kQ * 128 : 0)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        __syncwarp();
       }
+      const float mul = row_scale[h * kQ + row].x, addm = row_scale[h * kQ + row].y;  // score = mul * (acc, or fp32: scale_r acc + z_r addm)
       if (it.k0 < it.k1) {
         fence_async();
         mbar_arrive(&q_full);
@@ -870,43 +875,58 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const float sum_l = halves(l).x + halves(l).y, sum_z = halves(z).x + halves(z).y;
       const float inv = last ? (sum_l > 0.f || sum_l != sum_l ? 1.f / sum_l : 0.f) : 1.f;
       const float m_ref = m + (FP32 ? (float)(e_cur - 6) : 0.f);  // what l and the output are relative to
-      float* part = last ? nullptr : a.part + ((size_t)i * kItem + h * kQ + row) * (D + 4);
+      float* part = last ? nullptr : a.part + ((size_t)i * kItem + h * kQ) * (D + 4);
+      // 32 columns of the warp's 32 rows at a time through shared memory (q's place: its products are done), so that a row's
+      // bytes are written by neighbouring lanes
+      unsigned char* stage = smem + L::kQAt + h * L::kQTile + wrow0 * 128;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        float o[16], s[16];
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        f2 o[16], s[16];
         __syncwarp();
         if (n > 0) {
-          tmem_ld16(t_out + c, o);
-          if (FP32 && n > kFlush) tmem_ld16(t_sum + c, s);
+          tmem_ld32(t_out + c0, o);
+          if (FP32 && n > kFlush) tmem_ld32(t_sum + c0, s);
           tmem_wait_ld();
         }
+        const bool bad = (nan_groups >> (c0 >> 6)) & 1u;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (FP32 && n > kFlush) o[e] += s[e];
-          o[e] = n > 0 ? (FP32 ? o[e] + sum_z : o[e]) * inv : 0.f;
-          if (nan_groups >> (c >> 6) & 1u) o[e] = NAN;
-        }
-        if (on) {
-          float y0[8], y1[8];
+        for (int c = 0; c < 8; ++c) {
+          float4 v;
+          float* y = &v.x;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y0[e] = o[e];
-            y1[e] = o[8 + e];
+          for (int e = 0; e < 2; ++e) {
+            f2 x = n > 0 ? o[2 * c + e] : 0ull;
+            if (FP32 && n > kFlush) x = sum2(x, s[2 * c + e]);
+            if (FP32) x = sum2(x, pair_of(sum_z, sum_z));
+            const float2 u = halves(mul2(x, pair_of(inv, inv)));
+            y[2 * e] = bad ? NAN : n > 0 ? u.x : 0.f;
+            y[2 * e + 1] = bad ? NAN : n > 0 ? u.y : 0.f;
           }
-          if (last) {
-            const size_t at = (size_t)(sq.tok0 + tok) * a.a.ldo + (size_t)head * D + c;
-            store_out(a.a, at, y0);
-            store_out(a.a, at + 8, y1);
-          } else {
-            store8(part + c, y0);
-            store8(part + c + 8, y1);
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r8 = 0; r8 < 8; ++r8) {
+          const int r = r8 * 4 + (lane >> 3), c = lane & 7, t = (qrow0 + wrow0 + r) / a.by_grp, hd = it.h * a.grp + qrow0 + wrow0 + r - t * a.grp;
+          const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+          if (t < sq.c) {
+            const size_t at = (size_t)(sq.tok0 + t) * a.a.ldo + (size_t)hd * D + c0 + 4 * c;
+            if (!last) {
+              *reinterpret_cast<float4*>(part + (size_t)(wrow0 + r) * (D + 4) + c0 + 4 * c) = v;
+            } else if (FP32) {
+              *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.a.out) + at) = v;
+            } else {
+              const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y), q = __floats2bfloat162_rn(v.z, v.w);
+              *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.a.out) + at) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+            }
           }
         }
       }
       if (on) {
         if (!last) {
-          part[D] = m_ref;
-          part[D + 1] = sum_l;
+          part[(size_t)row * (D + 4) + D] = m_ref;
+          part[(size_t)row * (D + 4) + D + 1] = sum_l;
         } else if (a.lse != nullptr) {
           a.lse[(size_t)(sq.tok0 + tok) * a.g.nq + head] = sum_l > 0.f ? m_ref + log2f(sum_l) : INFINITY;
         }
