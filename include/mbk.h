@@ -387,11 +387,14 @@ int mbk_kv4_read(const mbk_kv4_config *cfg, const void *pool, int32_t layer, con
  *   s = scale * q . k_r;  cap > 0: s = cap * tanh(s / cap);  slopes: s += slopes[head] * (pos_r - pos_i)
  *   out = sum_r softmax(s)_r v_r;  zero for a token that sees no row
  * q and out: [n_tokens][n_heads][head_dim] in `dtype` with ldq, ldo elements between tokens (alignment as
- * append's).  Query head h reads KV head h / (n_heads / n_kv_heads).  slopes: DEVICE fp32 [n_heads] or NULL.
+ * append's); they must not overlap.  Query head h reads KV head h / (n_heads / n_kv_heads).  slopes: DEVICE
+ * fp32 [n_heads] or NULL.
  * accumulate (track = 1 only): adds to each row's weight the sum of softmax(s)_r over the sequence's new tokens and
  * the KV head's query heads.
  * Numerics: fp32 throughout for fp32 (operands of the tensor cores as fp16 pairs of 22 bits); for bf16 the
- * softmax weights are rounded to fp16.  Results do not depend on anything but the inputs and the GPU (no atomics).
+ * softmax weights (and, for prompts, the rows' values) are rounded to fp16.  A cap makes each score wrong by up to
+ * about 2^-22 of the cap, so it is meant for caps of tens or hundreds.  Results do not depend on anything but
+ * the inputs and the GPU (no atomics).
  * workspace: mbk_kv4_attention_workspace(cfg, batch) bytes (0 is possible), 16-byte aligned, contents arbitrary. */
 int64_t mbk_kv4_attention_workspace(const mbk_kv4_config *cfg, const mbk_kv4_batch *batch);
 int mbk_kv4_attention(const mbk_kv4_config *cfg, void *pool, int32_t layer, const mbk_kv4_batch *batch, const void *q,
@@ -400,7 +403,8 @@ int mbk_kv4_attention(const mbk_kv4_config *cfg, void *pool, int32_t layer, cons
 
 /* Eviction (track = 1): in each of layers [layer, layer + n_layers) and each KV head, of a sequence's
  * rows[s] rows at most `keep` are kept: first those with a position >= next_pos[s] - recent, then those of the
- * largest accumulated weight, the lower row first among equals (NaN counts as 0).  Kept rows below `keep`
+ * largest accumulated weight, the lower row first among equals (NaN counts as 0); a sequence whose rows[s] is
+ * outside [0, max_rows] is left as it is.  Kept rows below `keep`
  * stay where they are and the j-th row that became free gets the j-th kept row from above, so the order of
  * rows changes; their positions and weights go with them.  rows_out[s] = min(rows[s], keep) (it may be
  * rows itself).  out_tables NULL: in place; pages behind the first ceil(keep / page_size) are then free.

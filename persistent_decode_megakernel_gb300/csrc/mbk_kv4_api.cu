@@ -102,7 +102,10 @@ int mbk_kv4_read(const mbk_kv4_config* cfg, const void* pool, int32_t layer, con
 }
 
 int64_t mbk_kv4_attention_workspace(const mbk_kv4_config* cfg, const mbk_kv4_batch* batch) {
-  if (kv4_config_check(cfg) != MBK_OK || !batch || batch->n_tokens < 1) return MBK_ERR_INVALID_ARG;
+  if (kv4_config_check(cfg) != MBK_OK || !batch || batch->n_seq < 1 || batch->n_seq > MBK_KV4_MAX_SEQS || batch->n_tokens < 1 ||
+      batch->max_count < 1 || batch->max_count > batch->n_tokens || batch->max_rows < 0 ||
+      (int64_t)batch->max_rows > (int64_t)cfg->max_pages * cfg->page_size)
+    return MBK_ERR_INVALID_ARG;
   const int sms = sms_of(cfg->device);
   if (sms == 0) return MBK_ERR_UNSUPPORTED;
   return (int64_t)kv4_attention_workspace(kv4_geom(*cfg, nullptr), batch_of(*batch), sms);
@@ -113,8 +116,8 @@ int mbk_kv4_attention(const mbk_kv4_config* cfg, void* pool, int32_t layer, cons
                       int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!common_ok(cfg, pool, layer, dtype) || !batch_ok(*cfg, batch)) return MBK_ERR_INVALID_ARG;
   const int64_t row = (int64_t)cfg->n_heads * cfg->head_dim;
-  if (!rows_ok(q, ldq, row, dtype) || !rows_ok(out, ldo, row, dtype) || !std::isfinite(scale) || !(cap >= 0.f) || !std::isfinite(cap) ||
-      !aligned4(slopes) || window < 0 || (accumulate != 0 && accumulate != 1) || (accumulate && !cfg->track))
+  if (!rows_ok(q, ldq, row, dtype) || !rows_ok(out, ldo, row, dtype) || q == out || !std::isfinite(scale) ||
+      !(cap >= 0.f) || !std::isfinite(cap) || !aligned4(slopes) || window < 0 || (accumulate != 0 && accumulate != 1) || (accumulate && !cfg->track))
     return MBK_ERR_INVALID_ARG;
   // the split counts blocks of rows in 32 bits, tiles of 8 query rows at least
   const double tiles = std::ceil((double)batch->max_count * (cfg->n_heads / cfg->n_kv_heads) / 8.0);

@@ -227,7 +227,7 @@ struct EvictArgs {
   int32_t *rows_out, *status;
   int32_t* map;     // [segment][keep]
   int32_t* movers;  // [segment][keep]
-  int32_t* kept;    // [segment] rows that are left
+  int32_t* kept;    // [segment] rows that are left, or -1: the sequence's row count is out of bounds
 };
 
 template <int NT>
@@ -261,14 +261,15 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Evic
   const int seg = blockIdx.x, h = seg % a.g.nkv, s = seg / a.g.nkv % a.n_seq, layer = a.layer0 + seg / (a.g.nkv * a.n_seq);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int r = a.rows[s];
-  if (r < 0 || r > a.max_rows) {
-    if (tid == 0) flag(a.status, MBK_KV4_BAD_BATCH);
-    r = min(max(r, 0), a.max_rows);
-  }
+  const int r = a.rows[s];
+  const bool bad = r < 0 || r > a.max_rows;  // left as it is
   const int keep = a.keep;
   int32_t* map = a.map + (size_t)seg * keep;
-  if (tid == 0) a.kept[seg] = min(r, keep);
+  if (tid == 0) {
+    if (bad) flag(a.status, MBK_KV4_BAD_BATCH);
+    a.kept[seg] = bad ? -1 : min(r, keep);
+  }
+  if (bad) return;
   if (r <= keep) {
     for (int i = tid; i < r; i += NT) map[i] = i;
     return;
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(256) move_kernel(const __grid_constant__ Evict
   const int nb = (min(a.keep, a.max_rows) + kMove - 1) / kMove, seg = blockIdx.x / nb, rb = blockIdx.x - seg * nb;
   const int h = seg % a.g.nkv, s = seg / a.g.nkv % a.n_seq, layer = a.layer0 + seg / (a.g.nkv * a.n_seq);
   const int n = a.kept[seg], r0 = rb * kMove;
-  if (rb == 0 && h == 0 && layer == a.layer0 && threadIdx.x == 0) a.rows_out[s] = n;
+  if (rb == 0 && h == 0 && layer == a.layer0 && threadIdx.x == 0) a.rows_out[s] = n < 0 ? a.rows[s] : n;
   if (r0 >= n) return;
   const int rows = min(kMove, n - r0);
   if (threadIdx.x < rows) {

@@ -427,3 +427,176 @@ def test_decode_with_eviction_step_by_step():
             assert rows == [min(keep, r) for r in rows]
         counts = [1, 1]
     assert s.cache.status() == 0
+
+
+def test_many_sequences_take_the_block_wide_scan():
+    """More than 32 sequences (the split's scan over warps) and more than a block of threads, with idle slots among them."""
+    rng = np.random.default_rng(7)
+    for n in (33, 300):
+        rows = rng.integers(0, 5, n).tolist()
+        counts = [int(r > 0 and rng.random() < 0.8) for r in rows]
+        counts[0], rows[0] = 1, 3
+        s = Setup(rows, counts, 4, 2, 64, seed=n)
+        q = s.q(torch.float32)
+        want, _ = s.expect(q)
+        check(_run(s, q, {}), want, s.tolerance(q, torch.float32), str(n))
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1.0])
+@pytest.mark.parametrize("heads,dtype", [((4, 2, 64), torch.float32), ((8, 2, 128), torch.bfloat16)], ids=str)
+def test_scales(heads, dtype, scale):
+    s = Setup([60, 10, 150], [60, 1, 2], *heads)
+    q = s.q(dtype)
+    want, _ = plain.attention(s.pool, s.layer, q.double().numpy(), s.offsets, s.rows, s.tables, s.positions, s.heads, scale)
+    got = s.cache.attention(s.layer, s.batch, q.cuda(), scale=scale)
+    check(got, want, s.tolerance(q, dtype) * max(1.0, abs(scale) * s.d ** 0.5), str(scale))
+
+
+@pytest.mark.parametrize("heads,dtype", [((9, 3, 64), torch.float32), ((4, 2, 128), torch.bfloat16), ((4, 2, 128), torch.float32)], ids=str)
+@pytest.mark.parametrize("counts", [[10, 11, 12], [32, 33, 1], [17], [16], [8]], ids=str)
+def test_around_the_border_between_the_kernels(heads, dtype, counts):
+    """Query rows per KV head just below and above the prompt kernel's least, one sequence and several."""
+    s = Setup([c + 45 for c in counts], counts, *heads, track=True, gap=1)
+    q = s.q(dtype)
+    want, w = s.expect(q)
+    check(_run(s, q, {}, accumulate=True), want, s.tolerance(q, dtype), str(counts))
+    got = s.cache.weights.cpu()
+    for (b, i, h), x in list(w.items())[::5]:
+        page, blk, lane = int(s.tables[b][i // 32]), i % 32 // 32, i % 32
+        old = s.pool.weight(s.layer, s.tables[b], i, h)
+        assert abs(float(got[page, s.layer, h, blk, lane]) - old - x) <= 4 * s.tolerance(q, torch.float32) * x + 2.0 ** -23 * (old + x)
+
+
+def test_bounds_above_what_the_batch_holds():
+    """max_count, n_tokens and max_rows are bounds: a batch of prompts whose sequences turn out to be short."""
+    s = Setup([40, 70, 5], [1, 2, 0], 4, 2, 64)
+    q = s.q(torch.float32)
+    want, _ = s.expect(q)
+    for max_count in (3, 100, 200):
+        big = torch.zeros(200, 4, 64)
+        big[:3] = q
+        b = s.cache.batch(s.dev["offsets"], s.dev["rows"], s.dev["tables"], n_tokens=200, max_count=max_count, max_rows=96)
+        check(s.cache.attention(s.layer, b, big.cuda())[:3], want, s.tolerance(q, torch.float32), str(max_count))
+    one = Setup([70], [2], 4, 2, 64)
+    q = one.q(torch.float32)
+    want, _ = one.expect(q)
+    b = one.cache.batch(one.dev["offsets"], one.dev["rows"], one.dev["tables"], n_tokens=64, max_count=64)
+    big = torch.zeros(64, 4, 64)
+    big[:2] = q
+    check(one.cache.attention(one.layer, b, big.cuda())[:2], want, one.tolerance(q, torch.float32), "one")
+
+
+def test_graphs_of_split_calls_and_evictions_at_once():
+    """Two captured graphs (a long decode, a prompt; each with its own workspaces) replayed together on two streams, and an
+    eviction captured with them, give what eager calls give."""
+    a = Setup([3000, 900], [1, 1], 6, 2, 64, track=True, layers=1, layer=0, page=64)
+    b = Setup([600, 130], [100, 90], 4, 1, 128, page=64)
+    qa, qb = a.q(torch.float32).cuda(), b.q(torch.bfloat16).cuda()
+    nxt = torch.tensor([4000, 4000], dtype=torch.int32, device="cuda")
+    start = a.cache.pool.clone()
+    def step_a():
+        out = a.cache.attention(0, a.batch, qa, accumulate=True)
+        return out, a.cache.evict(a.dev["rows"], a.dev["tables"], nxt, 500, 10)
+    def step_b():
+        return b.cache.attention(b.layer, b.batch, qb)
+    want_a, want_rows = step_a()
+    want_pool, want_b = a.cache.pool.clone(), step_b()
+    graphs, outs, st = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for f in (step_a, step_b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for _ in range(5):
+        a.cache.pool.copy_(start)
+        torch.cuda.synchronize()
+        for g, stream in zip(graphs, st):
+            with torch.cuda.stream(stream):
+                g.replay()
+                if g is graphs[1]:
+                    g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0][0], want_a) and torch.equal(outs[0][1], want_rows) and torch.equal(outs[1], want_b)
+        assert torch.equal(a.cache.pool, want_pool)
+    assert a.cache.status() == 0 and b.cache.status() == 0
+
+
+def test_a_pool_of_more_than_four_gigabytes():
+    """Pages whose bytes lie beyond 2^32: append, read, attention, eviction there, and nothing written below."""
+    from persistent_decode_megakernel_gb300.kv4 import Kv4Cache
+    page, layers, kv, d = 1024, 8, 8, 128
+    per_page = layers * kv * page * 152
+    pages = 5 * 2 ** 30 // per_page + 3
+    cache = Kv4Cache(layers, 16, kv, d, pages, page, 2, True)
+    assert cache.bytes > 2 ** 32 + 2 * per_page
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    tables, n = dev([[pages - 1, pages - 2]]), 1100
+    b = cache.batch(dev([0, n]), dev([n]), tables, n_tokens=n, max_count=n)
+    k, v = torch.randn(n, kv, d, device="cuda"), torch.randn(n, kv, d, device="cuda")
+    cache.append(layers - 1, b, k, v)
+    k4, v4 = cache.read(layers - 1, b)
+    assert (k4 - k).abs().max() < 0.4 and (v4 - v).abs().max() < 0.4
+    q = torch.randn(n, 16, d, device="cuda", dtype=torch.bfloat16)
+    out = cache.attention(layers - 1, b, q, accumulate=True)
+    p = torch.einsum("qhd,khd->hqk", q.double(), k4.double().repeat_interleave(2, 1)) * d ** -0.5
+    p = p.masked_fill(torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1), -np.inf).softmax(-1)
+    want = torch.einsum("hqk,khd->qhd", p, v4.double().repeat_interleave(2, 1))
+    assert (out.double() - want).norm() / want.norm() < 2.0 ** -8 + 2.0 ** -9
+    rows = cache.evict(dev([n]), tables, dev([n]), 1000, 100, layer=layers - 1)
+    assert rows.tolist() == [1000] and cache.status() == 0
+    assert not cache.pool[:2 ** 32].any()
+
+
+def test_evict_of_more_rows_than_keys_fit_in_shared_memory():
+    """40,000 rows: the selection reads the weights again instead of keeping the keys."""
+    from persistent_decode_megakernel_gb300.kv4 import Kv4Cache
+    n, keep = 40000, 15000
+    cache = Kv4Cache(1, 1, 1, 64, 320, 128, 320, True)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    order = torch.randperm(320, generator=torch.Generator().manual_seed(1))
+    w = (torch.rand(n, generator=torch.Generator().manual_seed(2)) * 1000).round() / 8
+    w = torch.cat([w, torch.full((320 * 128 - n,), 1e9)])
+    cache.weights[order.cuda()] = w.view(320, 1, 1, 4, 32).cuda()
+    cache.positions[order.cuda()] = torch.arange(320 * 128, dtype=torch.int32).view(320, 1, 1, 4, 32).cuda()
+    rows = cache.evict(dev([n]), order.to(torch.int32).view(1, -1).cuda(), dev([n]), keep, 100)
+    src = plain.evict_map(w[:n].tolist(), list(range(n)), keep, n - 100)
+    assert rows.tolist() == [keep]
+    assert torch.equal(cache.positions.cpu()[order].flatten()[:keep], torch.tensor(src, dtype=torch.int32))
+
+
+def test_evict_leaves_a_sequence_with_a_bad_row_count_alone():
+    from persistent_decode_megakernel_gb300 import mbk
+    s = Setup([100, 90], [1, 1], 4, 2, 64, track=True)
+    before = s.bytes().copy()
+    rows = torch.tensor([10 ** 6, 90], dtype=torch.int32, device="cuda")
+    got = s.cache.evict(rows, s.dev["tables"], rows, 32, layer=s.layer, max_rows=128)
+    assert got.tolist() == [10 ** 6, 32] and s.cache.status() == mbk.MBK_KV4_BAD_BATCH
+    for page in s.tables[0][:4]:
+        assert (s.bytes()[page] == before[page]).all()
+
+
+def test_tensors_refused():
+    s = Setup([40], [1], 4, 2, 64)
+    q = s.q(torch.float32).cuda()
+    wide = torch.zeros(2, 4, 130, device="cuda")
+    for bad in (q.cpu(), q.half(), q[0], q.expand(2, 4, 64), wide[:1, :, 1:65], wide[:1, :, :64], q.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            s.cache.attention(s.layer, s.batch, bad)
+    with pytest.raises(ValueError):
+        s.cache.attention(s.layer, s.batch, q, out=torch.empty(1, 4, 64, device="cuda", dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        s.cache.attention(s.layer, s.batch, q, slopes=torch.zeros(3, device="cuda"))
+    from persistent_decode_megakernel_gb300 import mbk
+    for kw in (dict(out=q), dict(accumulate=True), dict(window=-1), dict(cap=-1.0), dict(scale=float("nan"))):
+        with pytest.raises(mbk.MbkError):
+            s.cache.attention(s.layer, s.batch, q, **kw)
+    for layer in (-1, 2):
+        with pytest.raises(mbk.MbkError):
+            s.cache.attention(layer, s.batch, q)
+    k = torch.zeros(1, 2, 64, device="cuda")
+    with pytest.raises(ValueError):
+        s.cache.append(0, s.batch, k, k.bfloat16())
+    with pytest.raises(ValueError):
+        s.cache.batch(s.dev["offsets"].long(), s.dev["rows"], s.dev["tables"])
+    with pytest.raises(ValueError):
+        s.cache.batch(s.dev["offsets"], s.dev["rows"], s.dev["tables"][:, :1])

@@ -57,8 +57,9 @@ def _append(lib, c=None, pool=P, layer=0, b=None, k=P, v=P, ld=128, dtype=0, fn=
 
 
 def _attention(lib, c=None, pool=P, layer=0, b=None, q=P, ldq=512, out=P, ldo=512, dtype=0, scale=1.0, cap=0.0, slopes=None, window=0,
-               accumulate=0, ws=P, size=1 << 40):
+               accumulate=0, ws=P, size=1 << 40, same=False):
     c, b = c or config(), b or batch()
+    out = out + 0x1000000 if out == q and not same else out
     return lib.mbk_kv4_attention(ctypes.byref(c), pool, layer, ctypes.byref(b), q, ldq, out, ldo, dtype, scale, cap, slopes, window, accumulate,
                                  ws, size, None)
 
@@ -84,7 +85,7 @@ def test_rows_refused(lib, bad):
 @pytest.mark.parametrize("bad", [dict(pool=None), dict(layer=2), dict(q=None), dict(out=None), dict(q=P + 4), dict(ldq=508), dict(ldo=514),
                                  dict(dtype=3), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0), dict(cap=float("nan")),
                                  dict(cap=float("inf")), dict(slopes=P + 1), dict(window=-1), dict(accumulate=2),
-                                 dict(accumulate=1, c=config(track=0)),
+                                 dict(accumulate=1, c=config(track=0)), dict(same=True),
                                  dict(b=batch(n_seq=1024, n_tokens=1 << 30, max_count=1 << 30))], ids=lambda b: "-".join(b))
 def test_attention_refused(lib, bad):
     assert _attention(lib, **bad) == mbk.MBK_ERR_INVALID_ARG
