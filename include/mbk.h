@@ -383,14 +383,15 @@ int mbk_kv4_read(const mbk_kv4_config *cfg, const void *pool, int32_t layer, con
 
 /* Attention of the new tokens over their sequences' rows of `layer`: token i of a sequence with c new
  * tokens and R rows sees rows r <= R - c + i, and of these with window > 0 only those whose position is
- * less than `window` before its own.  Positions are the stored ones (track = 1) or the row's index.
+ * less than `window` before its own.  Positions are the stored ones (track = 1) or the row's index; they are not
+ * negative.
  *   s = scale * q . k_r;  cap > 0: s = cap * tanh(s / cap);  slopes: s += slopes[head] * (pos_r - pos_i)
  *   out = sum_r softmax(s)_r v_r;  zero for a token that sees no row
  * q and out: [n_tokens][n_heads][head_dim] in `dtype` with ldq, ldo elements between tokens (alignment as
  * append's); they must not overlap.  Query head h reads KV head h / (n_heads / n_kv_heads).  slopes: DEVICE
  * fp32 [n_heads] or NULL.
  * accumulate (track = 1 only): adds to each row's weight the sum of softmax(s)_r over the sequence's new tokens and
- * the KV head's query heads.
+ * the KV head's query heads; no two sequences of such a call may share a page.
  * Numerics: fp32 throughout for fp32 (operands of the tensor cores as fp16 pairs of 22 bits); for bf16 the
  * softmax weights (and, for prompts, the rows' values) are rounded to fp16.  A cap makes each score wrong by up to
  * about 2^-22 of the cap, so it is meant for caps of tens or hundreds.  Results do not depend on anything but

@@ -1,5 +1,7 @@
 // mbk_kv4_rows.cu -- the 4-bit KV cache's rows: append (quantise), read, and eviction by accumulated
 // attention weight.  Also the pool's geometry.
+#include <climits>
+
 #include "mbk_kv4_device.h"
 
 namespace mbk {
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Evic
     return;
   }
   const int32_t* table = a.tables + (size_t)s * a.g.max_pages;
-  const int young = a.next_pos[s] - a.recent;
+  const int young = max(a.next_pos[s], INT_MIN + a.recent) - a.recent;
   const int words = (r + 31) / 32, all_words = (a.max_rows + 31) / 32;
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem);             // kept rows
   int* ranks = reinterpret_cast<int*>(bits + all_words);          // [all_words + 1] free rows (kept rows from `keep` on) before a word

@@ -22,7 +22,6 @@ import torch
 from . import mbk
 
 
-
 def _raw_stream(index: int) -> int:
     """The handle of torch's current stream of a device."""
     return torch._C._cuda_getCurrentRawStream(index)  # torch.cuda.current_stream makes an object first: 2 us more
@@ -37,9 +36,10 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 class Kv4Batch:
     """The tokens of a call (mbk_kv4_batch).  It keeps its tensors; their contents may change between
-    calls within the bounds that it was made with, their addresses may not."""
+    calls within the bounds that it was made with, their addresses may not.  It serves the cache that made it."""
 
-    def __init__(self, c: mbk.MbkKv4Batch, keep, workspace_bytes: int):
+    def __init__(self, cache: "Kv4Cache", c: mbk.MbkKv4Batch, keep, workspace_bytes: int):
+        self.cache = cache  # its bounds and tables are of this cache's shape
         self.c = c
         self.ref = ctypes.byref(c)
         self.keep = keep
@@ -96,6 +96,11 @@ class Kv4Cache:
             raise ValueError(f"{name}: 16-byte aligned")
         return p, ld
 
+    def _own(self, batch: Kv4Batch):
+        if batch.cache is not self:
+            raise ValueError("batch: of this cache (Kv4Cache.batch)")
+        return batch.ref
+
     def _stream(self) -> int:
         return _raw_stream(self.index)
 
@@ -123,7 +128,7 @@ class Kv4Cache:
                 0 <= max_rows <= self.cfg.max_pages * self.cfg.page_size):
             raise mbk.MbkError(mbk.MBK_ERR_INVALID_ARG, "Kv4Cache.batch")
         size = self._size(self.lib.mbk_kv4_attention_workspace(self._cfg, ctypes.byref(c)), "mbk_kv4_attention_workspace")
-        return Kv4Batch(c, (offsets, rows, tables, positions, status), size)
+        return Kv4Batch(self, c, (offsets, rows, tables, positions, status), size)
 
     def append(self, layer: int, batch: Kv4Batch, k, v) -> None:
         """Store the new tokens' rows (mbk_kv4_append)."""
@@ -131,7 +136,7 @@ class Kv4Cache:
         vp, ldv = self._rows("v", v, batch.n_tokens, self.cfg.n_kv_heads)
         if ld != ldv or k.dtype != v.dtype:
             raise ValueError("k and v: one type and one distance between tokens")
-        mbk._check(self.lib.mbk_kv4_append(self._cfg, self._pool, layer, batch.ref, kp, vp, ld, _DTYPES[k.dtype], self._stream()),
+        mbk._check(self.lib.mbk_kv4_append(self._cfg, self._pool, layer, self._own(batch), kp, vp, ld, _DTYPES[k.dtype], self._stream()),
                    "mbk_kv4_append")
 
     def read(self, layer: int, batch: Kv4Batch, dtype=torch.float32):
@@ -141,7 +146,7 @@ class Kv4Cache:
         shape = (batch.n_tokens, self.cfg.n_kv_heads, self.cfg.head_dim)
         k = torch.empty(shape, dtype=dtype, device=self.device)
         v = torch.empty(shape, dtype=dtype, device=self.device)
-        mbk._check(self.lib.mbk_kv4_read(self._cfg, self._pool, layer, batch.ref, k.data_ptr(), v.data_ptr(), shape[1] * shape[2],
+        mbk._check(self.lib.mbk_kv4_read(self._cfg, self._pool, layer, self._own(batch), k.data_ptr(), v.data_ptr(), shape[1] * shape[2],
                                          _DTYPES[dtype], self._stream()), "mbk_kv4_read")
         return k, v
 
@@ -161,7 +166,7 @@ class Kv4Cache:
                                    slopes.shape != (cfg.n_heads,)):
             raise ValueError(f"slopes: a contiguous fp32 tensor {(cfg.n_heads,)} on {self.device}")
         ws = torch.empty(batch.workspace_bytes, dtype=torch.uint8, device=self.device) if batch.workspace_bytes else None
-        rc = self.lib.mbk_kv4_attention(self._cfg, self._pool, layer, batch.ref, qp, ldq, op, ldo, _DTYPES[q.dtype],
+        rc = self.lib.mbk_kv4_attention(self._cfg, self._pool, layer, self._own(batch), qp, ldq, op, ldo, _DTYPES[q.dtype],
                                         cfg.head_dim ** -0.5 if scale is None else scale, cap, _ptr(slopes), window, int(accumulate),
                                         _ptr(ws), batch.workspace_bytes, _raw_stream(self.index))
         if rc != mbk.MBK_OK:

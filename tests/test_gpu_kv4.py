@@ -600,3 +600,83 @@ def test_tensors_refused():
         s.cache.batch(s.dev["offsets"].long(), s.dev["rows"], s.dev["tables"])
     with pytest.raises(ValueError):
         s.cache.batch(s.dev["offsets"], s.dev["rows"], s.dev["tables"][:, :1])
+
+
+def test_a_batch_of_another_cache_is_refused():
+    a, b = Setup([40], [1], 4, 2, 64), Setup([400], [1], 4, 2, 64)
+    q, k = torch.zeros(1, 4, 64, device="cuda"), torch.zeros(1, 2, 64, device="cuda")
+    for call in (lambda: b.cache.attention(0, a.batch, q), lambda: b.cache.append(0, a.batch, k, k), lambda: b.cache.read(0, a.batch)):
+        with pytest.raises(ValueError):
+            call()
+
+
+PROMPTS = [((4, 2, 64), torch.float32), ((4, 2, 128), torch.bfloat16), ((4, 2, 128), torch.float32)]
+
+
+@pytest.mark.parametrize("window", [0, 10])
+@pytest.mark.parametrize("heads,dtype", PROMPTS, ids=str)
+def test_nan_rows_under_a_prompt(heads, dtype, window):
+    """The last group of V is NaN in row 70, K in row 93: each query's dims are NaN exactly where it sees them."""
+    s = Setup([100], [60], *heads)
+    for row, k_bad in ((70, False), (93, True)):
+        for h in range(s.kv):
+            k, v = (x.astype(np.float32) for x in s.pool.get(s.layer, s.tables[0], row, h))
+            (k if k_bad else v)[-64:] = np.nan
+            s.pool.put(s.layer, s.tables[0], row, h, k, v)
+    s.cache.pool.copy_(torch.from_numpy(s.pool.bytes.reshape(-1)))
+    q = s.q(dtype)
+    want, _ = s.expect(q, window=window)
+    got = s.cache.attention(s.layer, s.batch, q.cuda(), window=window).double().cpu().numpy()
+    assert (np.isnan(got) == np.isnan(want)).all()
+    good = Setup([70], [30], *heads)  # the tolerance of the rows before them, whose values are of the same size
+    check(torch.from_numpy(np.nan_to_num(got)), np.nan_to_num(want), good.tolerance(q, dtype), "others")
+
+
+@pytest.mark.parametrize("heads,dtype", PROMPTS, ids=str)
+def test_more_new_tokens_than_rows(heads, dtype):
+    """The first tokens see no row: zero; a sequence without rows and one that sees all."""
+    s = Setup([20, 0, 70], [60, 40, 50], *heads)
+    q = s.q(dtype)
+    want, _ = s.expect(q)
+    assert (want[:40] == 0).all() and (want[60:100] == 0).all()
+    check(_run(s, q, {}), want, s.tolerance(q, dtype), "out")
+
+
+@pytest.mark.parametrize("heads,dtype", PROMPTS, ids=str)
+def test_prompts_inside_wider_rows(heads, dtype):
+    s = Setup([90, 40], [60, 33], *heads)
+    n, nq, d = s.offsets[-1], s.heads, s.d
+    wide = torch.randn(n, nq + 3, d, device="cuda").to(dtype)
+    out = torch.full((n, nq + 2, d), 7.0, device="cuda", dtype=dtype)
+    s.cache.attention(s.layer, s.batch, wide[:, 1:1 + nq], out=out[:, 2:])
+    assert (out[:, :2] == 7).all()
+    assert torch.equal(out[:, 2:], s.cache.attention(s.layer, s.batch, wide[:, 1:1 + nq].contiguous()))
+
+
+@pytest.mark.parametrize("count", [1, 50])
+@pytest.mark.parametrize("heads,dtype", PROMPTS, ids=str)
+def test_values_at_the_end_of_fp16(heads, dtype, count):
+    """K and V up to +-65504 (a scale that is rounded up may lead lo + 15 scale beyond it)."""
+    s = Setup([80], [count], *heads, fill=False)
+    for i in range(80):
+        for h in range(s.kv):
+            k, v = s.rng.uniform(-65504, 65504, size=(2, s.d)).astype(np.float32)
+            k[0], k[1], v[0], v[1] = 65504, -65504, 65504, -65504
+            s.pool.put(s.layer, s.tables[0], i, h, k, v)
+    s.cache.pool.copy_(torch.from_numpy(s.pool.bytes.reshape(-1)))
+    q, scale = s.q(dtype), 1e-6
+    want, _ = plain.attention(s.pool, s.layer, q.double().numpy(), s.offsets, s.rows, s.tables, None, s.heads, scale)
+    size = float(q.double().norm(dim=-1).max()) * 65504 * s.d ** 0.5 * scale
+    tol = size * (2.0 ** -22 + s.d ** 0.5 * 2.0 ** -23) + 2.0 ** -19
+    if dtype == torch.bfloat16:  # prompts: K and V are rounded to fp16 too, off by 2^-11 of themselves (independent from row to row)
+        tol += 2.0 ** -8 + 2 * 2.0 ** -11 + size * 2.0 ** -11
+    check(s.cache.attention(s.layer, s.batch, q.cuda(), scale=scale), want, tol, str(count))
+
+
+def test_evict_when_everything_is_recent():
+    """next_pos - recent below the least int: every row counts as recent, and the lowest rows are kept."""
+    s = Setup([100], [1], 4, 2, 64, track=True)
+    nxt = torch.tensor([-2 ** 31 + 3], dtype=torch.int32, device="cuda")
+    before = s.bytes().copy()
+    assert s.cache.evict(s.dev["rows"], s.dev["tables"], nxt, 50, 20, layer=s.layer).tolist() == [50]
+    assert (s.bytes() == before).all()
