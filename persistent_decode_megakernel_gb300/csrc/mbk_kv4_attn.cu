@@ -995,10 +995,14 @@ constexpr int kPromptRows = 33;
 bool has_prompts(const Kv4Geom& g, const Kv4Batch& b, int bf16) {
   return (long long)b.max_count * (g.nq / g.nkv) >= kPromptRows && (bf16 || g.d == 64);
 }
-size_t part_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
+// The workspace: the decode kernel's partials, the prompt kernel's, lse.
+size_t own_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
   // none where one CTA's warps have a block each, whatever the queries' type (tiles of 4 at least)
-  const size_t own = max_units(g, b, 4) <= (g.d == 64 ? 16 : 8) ? 0 : round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
-  return own + ((long long)b.max_count * (g.nq / g.nkv) >= kPromptRows ? round256(kv4_prompt_partials(g, b, num_sms)) : 0);
+  return max_units(g, b, 4) <= (g.d == 64 ? 16 : 8) ? 0 : round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);
+}
+size_t part_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
+  return own_bytes(g, b, num_sms) +
+         ((long long)b.max_count * (g.nq / g.nkv) >= kPromptRows ? round256(kv4_prompt_partials(g, b, num_sms)) : 0);
 }
 
 }  // namespace
@@ -1026,7 +1030,7 @@ cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const 
   if (prompts) {
     // a sequence alone goes to the prompt kernel however few its tokens turn out to be
     a.below = b.n_seq == 1 ? 1 : kPromptRows;
-    uint8_t* part = reinterpret_cast<uint8_t*>(ws) + round256((size_t)num_sms * 2 * 16 * (g.d + 4) * 4);  // (a prompt has many units)
+    uint8_t* part = reinterpret_cast<uint8_t*>(ws) + own_bytes(g, b, num_sms);
     if (cudaError_t e = kv4_prompt(g, layer, b, at, a.below, reinterpret_cast<float*>(part), a.lse, num_sms, st)) return e;
   }
   const bool others = !prompts || b.n_seq > 1;

@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   using L = Layout<D, FP32>;
   constexpr int kGroups = D / 64;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], pv_done[2][2], p_full[2], q_full, drain;  // [query tile][stage]
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], pv_done[2][2], p_full[2][2], q_full, drain;  // [query tile][stage]
   __shared__ uint32_t tmem_slot;
   __shared__ unsigned failed;
   __shared__ TileNote notes[kNotes];
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       for (int h = 0; h < 2; ++h) {
         mbar_init(&s_full[h][i], 2);
         mbar_init(&pv_done[h][i], 1);
+        mbar_init(&p_full[h][i], 128);
       }
-      mbar_init(&p_full[i], 128);
     }
     mbar_init(&q_full, 256);
     mbar_init(&drain, 1);
@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const bool fresh = FP32 ? j % kFlush == 0 : j == 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!warp_wait(&p_full[h], no & 1, abort)) return false;
+        // (a barrier a stage: a query tile may be done with the next key tile's weights before the other's are here)
+        if (!warp_wait(&p_full[h][no & 1], (no >> 1) & 1, abort)) return false;
         fence_after();
         if (no & 1) product_at(Const<1>{}, h, fresh); else product_at(Const<0>{}, h, fresh);
       }
@@ -862,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         tmem_wait_st();
         fence_before();
-        mbar_arrive(&p_full[h]);
+        mbar_arrive(&p_full[h][st]);
       }
       if (!ok) break;
       const int n = it.k1 - it.k0;

@@ -980,26 +980,24 @@ struct Kv4Step {
 // Grows the 4-bit cache's workspace to this call and copies the batch's arrays to it.  tables: DEVICE.
 int prepare_kv4(const PrefillModel& m, PrefillState& s, int n, const PrefillBatch& b, const int32_t* tables, cudaStream_t st, Kv4Step* out) {
   if (b.n_seq > kKv4MaxSeqs) return MBK_ERR_INVALID_ARG;
-  std::vector<int32_t> img;
-  img.reserve((size_t)3 * b.n_seq + 1);
+  int32_t img[3 * kKv4MaxSeqs + 1];  // offsets [n_seq + 1], rows [n_seq], positions [n_seq]
   int max_count = 1, max_rows = 1;
-  img.push_back(0);
+  img[0] = 0;
   for (int q = 0; q < b.n_seq; ++q) {
-    img.push_back(img.back() + b.counts[q]);
+    const int rows = (b.held != nullptr ? b.held[q] : b.starts[q]) + b.counts[q];
+    img[q + 1] = img[q] + b.counts[q];
+    img[b.n_seq + 1 + q] = rows;
+    img[2 * b.n_seq + 1 + q] = b.starts[q];
     max_count = std::max(max_count, (int)b.counts[q]);
+    max_rows = std::max(max_rows, rows);
   }
-  for (int q = 0; q < b.n_seq; ++q) {
-    img.push_back((b.held != nullptr ? b.held[q] : b.starts[q]) + b.counts[q]);
-    max_rows = std::max(max_rows, (int)img.back());
-  }
-  for (int q = 0; q < b.n_seq; ++q) img.push_back(b.starts[q]);
   Kv4Batch& kb = out->batch;
   kb.n_seq = b.n_seq;
   kb.n_tokens = n;
   kb.max_count = max_count;
   kb.max_rows = max_rows;
   const size_t qd = (size_t)m.nq * m.d;
-  const size_t b_int = round256(sizeof(int32_t) * img.size()), b_out = round256(sizeof(float) * (size_t)n * qd);
+  const size_t bytes = sizeof(int32_t) * (3 * (size_t)b.n_seq + 1), b_int = round256(bytes), b_out = round256(sizeof(float) * (size_t)n * qd);
   const size_t need = b_int + b_out + kv4_attention_workspace(*m.kv4, kb, m.num_sms);
   if (need > s.kv4_cap) {
     if (s.kv4_ws != nullptr) cudaFree(s.kv4_ws);
@@ -1010,7 +1008,7 @@ int prepare_kv4(const PrefillModel& m, PrefillState& s, int n, const PrefillBatc
   }
   unsigned char* w = reinterpret_cast<unsigned char*>(s.kv4_ws);
   int32_t* ints = reinterpret_cast<int32_t*>(w);
-  if (cudaMemcpyAsync(ints, img.data(), sizeof(int32_t) * img.size(), cudaMemcpyHostToDevice, st) != cudaSuccess) return MBK_ERR_CUDA;
+  if (cudaMemcpyAsync(ints, img, bytes, cudaMemcpyHostToDevice, st) != cudaSuccess) return MBK_ERR_CUDA;
   kb.offsets = ints;
   kb.rows = ints + b.n_seq + 1;
   kb.positions = m.kv4->track ? ints + 2 * b.n_seq + 1 : nullptr;  // an untracked cache was never cut: rows are positions

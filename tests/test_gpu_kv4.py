@@ -680,3 +680,46 @@ def test_evict_when_everything_is_recent():
     before = s.bytes().copy()
     assert s.cache.evict(s.dev["rows"], s.dev["tables"], nxt, 50, 20, layer=s.layer).tolist() == [50]
     assert (s.bytes() == before).all()
+
+
+def _random_cache(heads, kv, d, seqs, rows, counts, dtype, layers=1):
+    """A cache of normal rows (pages in order), a batch of the last `counts` tokens of each sequence, and queries."""
+    from persistent_decode_megakernel_gb300.kv4 import Kv4Cache
+    per = -(-rows // 64)
+    cache = Kv4Cache(layers, heads, kv, d, seqs * per, 64, per)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    tables, held = dev(list(range(seqs * per))).view(seqs, per), dev([rows] * seqs)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    every = cache.batch(dev([i * rows for i in range(seqs + 1)]), held, tables, n_tokens=seqs * rows, max_count=rows)
+    k, v = (torch.randn(seqs * rows, kv, d, device="cuda", generator=g) for _ in range(2))
+    cache.append(0, every, k, v)
+    n = sum(counts)
+    off = dev([0] + np.cumsum(counts).tolist())
+    batch = cache.batch(off, held, tables, n_tokens=n, max_count=max(counts), max_rows=rows)
+    q = torch.randn(n, heads, d, device="cuda", generator=g).to(dtype)
+    return cache, every, batch, q
+
+
+@pytest.mark.parametrize("counts", [[30] * 16, [32] * 15 + [50], [64, 33] * 8], ids=["half", "mixed", "uneven"])
+@pytest.mark.parametrize("heads,dtype", [((32, 8, 64), torch.bfloat16), ((32, 8, 128), torch.bfloat16), ((32, 8, 64), torch.float32)], ids=str)
+def test_query_tiles_that_run_ahead_of_each_other(heads, dtype, counts):
+    """Prompts whose second query tile is empty or short get through its keys much faster than the first: many calls
+    end without a wait that gives up, and all give the same."""
+    nq, kv, d = heads
+    rows = 4096
+    cache, every, batch, q = _random_cache(nq, kv, d, len(counts), rows, counts, dtype)
+    first = cache.attention(0, batch, q)
+    assert cache.status() == 0
+    for _ in range(60):
+        out = cache.attention(0, batch, q)
+    assert cache.status() == 0 and torch.equal(out, first)
+    k, v = (x.view(len(counts), rows, kv, d).double() for x in cache.read(0, every))
+    at = 0
+    for s, c in list(enumerate(counts))[::5]:
+        at = sum(counts[:s])
+        x = torch.einsum("qhgd,khd->hgqk", q[at:at + c].double().view(c, kv, nq // kv, d), k[s]) * d ** -0.5
+        x = x.masked_fill(torch.ones(c, rows, dtype=torch.bool, device="cuda").triu(rows - c + 1), -np.inf).softmax(-1)
+        want = torch.einsum("hgqk,khd->qhgd", x, v[s]).reshape(c, nq, d)
+        # scores below 8 in size: weights off by 8 (2^-22 + 11 2^-23); bf16: out 2^-8, weights and V 2^-11 each, K 2^-11 of a score's terms
+        tol = 2.0 ** -16 if dtype == torch.float32 else 2.0 ** -8 + 3 * 2.0 ** -11
+        assert (first[at:at + c].double() - want).norm() <= tol * want.norm()
