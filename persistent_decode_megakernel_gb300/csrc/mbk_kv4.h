@@ -53,7 +53,7 @@ size_t kv4_evict_workspace(const Kv4Geom& g, int n_layers, int n_seq, int keep);
 cudaError_t kv4_append(const Kv4Geom& g, int layer, const Kv4Batch& b, const void* k, const void* v, long long ld, int bf16,
                        cudaStream_t st);
 cudaError_t kv4_read(const Kv4Geom& g, int layer, const Kv4Batch& b, void* k, void* v, long long ld, int bf16, cudaStream_t st);
-cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4Attn& a, void* ws, int num_sms, cudaStream_t st);
+cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, Kv4Attn a, void* ws, int num_sms, cudaStream_t st);
 // The prompt kernel: the batch's sequences of at least `least` query rows per KV head (bf16, or fp32 with d 64).  part:
 // kv4_prompt_partials bytes; lse: [n_tokens][nq] or null.
 size_t kv4_prompt_partials(const Kv4Geom& g, const Kv4Batch& b, int num_sms);
@@ -61,7 +61,7 @@ cudaError_t kv4_prompt(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4
                        cudaStream_t st);
 cudaError_t kv4_evict(const Kv4Geom& g, int layer0, int n_layers, int n_seq, int max_rows, const int32_t* rows,
                       const int32_t* tables, const int32_t* next_pos, int keep, int recent, const int32_t* out_tables,
-                      int out_pages, int32_t* rows_out, int32_t* status, void* ws, cudaStream_t st);
+                      int out_pages, int32_t* rows_out, int32_t* status, void* ws, int num_sms, cudaStream_t st);
 
 // MBK_OK, or MBK_ERR_INVALID_ARG for a configuration that the kernels do not take.
 int kv4_config_check(const mbk_kv4_config* c);

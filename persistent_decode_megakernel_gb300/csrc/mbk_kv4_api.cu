@@ -117,7 +117,8 @@ int mbk_kv4_attention(const mbk_kv4_config* cfg, void* pool, int32_t layer, cons
   if (!common_ok(cfg, pool, layer, dtype) || !batch_ok(*cfg, batch)) return MBK_ERR_INVALID_ARG;
   const int64_t row = (int64_t)cfg->n_heads * cfg->head_dim;
   if (!rows_ok(q, ldq, row, dtype) || !rows_ok(out, ldo, row, dtype) || q == out || !std::isfinite(scale) ||
-      !(cap >= 0.f) || !std::isfinite(cap) || !aligned4(slopes) || window < 0 || (accumulate != 0 && accumulate != 1) || (accumulate && !cfg->track))
+      !(cap >= 0.f) || !std::isfinite(cap) || !aligned4(slopes) || window < 0 || (accumulate != 0 && accumulate != 1) ||
+      (accumulate && !cfg->track))
     return MBK_ERR_INVALID_ARG;
   // the split counts blocks of rows in 32 bits, tiles of 8 query rows at least
   const double tiles = std::ceil((double)batch->max_count * (cfg->n_heads / cfg->n_kv_heads) / 8.0);
@@ -146,8 +147,8 @@ int mbk_kv4_evict(const mbk_kv4_config* cfg, void* pool, int32_t layer, int32_t 
                   const int32_t* out_tables, int32_t out_pages, int32_t* rows_out, int32_t* status, void* workspace,
                   int64_t workspace_bytes, void* stream) {
   if (!common_ok(cfg, pool, layer, MBK_KV4_FP32) || !cfg->track || n_layers < 1 || n_layers > cfg->n_layers - layer || n_seq < 1 ||
-      n_seq > MBK_KV4_MAX_SEQS || max_rows < 1 || max_rows > MBK_KV4_MAX_EVICT_ROWS || (int64_t)max_rows > (int64_t)cfg->max_pages * cfg->page_size || !rows || !tables ||
-      !next_pos || !rows_out || keep < 1 || (int64_t)keep > (int64_t)cfg->max_pages * cfg->page_size || recent < 0 || recent > keep)
+      n_seq > MBK_KV4_MAX_SEQS || max_rows < 1 || max_rows > MBK_KV4_MAX_EVICT_ROWS ||
+      (int64_t)max_rows > (int64_t)cfg->max_pages * cfg->page_size || !rows || !tables || !next_pos || !rows_out || keep < 1 || (int64_t)keep > (int64_t)cfg->max_pages * cfg->page_size || recent < 0 || recent > keep)
     return MBK_ERR_INVALID_ARG;
   if (!aligned4(rows) || !aligned4(tables) || !aligned4(next_pos) || !aligned4(out_tables) || !aligned4(rows_out) || !aligned4(status))
     return MBK_ERR_INVALID_ARG;
@@ -157,11 +158,12 @@ int mbk_kv4_evict(const mbk_kv4_config* cfg, void* pool, int32_t layer, int32_t 
   const Kv4Geom g = kv4_geom(*cfg, pool);
   if (!workspace || !aligned16(workspace) || workspace_bytes < (int64_t)kv4_evict_workspace(g, n_layers, n_seq, keep))
     return MBK_ERR_INVALID_ARG;
-  if (sms_of(cfg->device) == 0) return MBK_ERR_UNSUPPORTED;
+  const int sms = sms_of(cfg->device);
+  if (sms == 0) return MBK_ERR_UNSUPPORTED;
   DeviceScope d(cfg->device);
   if (!d.ok) return MBK_ERR_CUDA;
   return launched(kv4_evict(g, layer, n_layers, n_seq, max_rows, rows, tables, next_pos, keep, recent, out_tables, out_pages, rows_out,
-                            status, workspace, (cudaStream_t)stream));
+                            status, workspace, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

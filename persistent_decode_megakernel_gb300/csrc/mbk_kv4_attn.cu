@@ -126,23 +126,23 @@ __device__ Split<TILE> make_split(const AttnArgs& a, SeqInfo* info, int* warp_su
     carry = __shfl_sync(0xffffffffu, x, 31);
     __syncwarp();
   } else {
-  for (int s0 = 0; s0 < a.b.n_seq; s0 += blockDim.x) {
-    const int s = s0 + threadIdx.x;
-    SeqInfo q{0, 0, 0, 0};
-    int n = 0;
-    if (s < a.b.n_seq) {
-      const SeqView v = seq_view(a.g, a.b, s, report);
-      q.r = v.r;
-      q.c = a.below == 0 || v.c * a.grp < a.below ? v.c : 0;  // longer ones are the prompt kernel's
-      q.tok0 = v.tok0;
-      n = sp.units(q);
+    for (int s0 = 0; s0 < a.b.n_seq; s0 += blockDim.x) {
+      const int s = s0 + threadIdx.x;
+      SeqInfo q{0, 0, 0, 0};
+      int n = 0;
+      if (s < a.b.n_seq) {
+        const SeqView v = seq_view(a.g, a.b, s, report);
+        q.r = v.r;
+        q.c = a.below == 0 || v.c * a.grp < a.below ? v.c : 0;
+        q.tok0 = v.tok0;
+        n = sp.units(q);
+      }
+      int total;
+      q.cum = carry + block_scan(n, warp_sums, &total);
+      if (s < a.b.n_seq) info[s] = q;
+      carry += total;
     }
-    int total;
-    q.cum = carry + block_scan(n, warp_sums, &total);
-    if (s < a.b.n_seq) info[s] = q;
-    carry += total;
-  }
-  __syncthreads();
+    __syncthreads();
   }
   sp.total = carry;
   // one block for each warp of a CTA before a second CTA is used
@@ -572,7 +572,11 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
     }
     // The block's share is summed from zero and added in fp32: the tensor cores' own sums are truncated, and
     // over thousands of rows that bias showed (3e-4).  For fp32 they also start at -7.5 sum(p), so that
-    // codes count from their middle: sum p (code - 7.5) is of the output's size, sum p code many times that.
+    // codes count from their middle: sum p (code - 7.5) is of the output's size, sum p code many times that.  Truncation
+    // leaves a bias in each block's share all the same, which grew against the output as its rows' average shrinks (9e-6 at
+    // 130,001 rows); so every other block takes 15 - code and is subtracted, and the biases cancel.
+    const float sign = P::kPrecise && (blk & 1) ? -1.f : 1.f;
+    const uint32_t flip = P::kPrecise && (blk & 1) ? ~0u : 0u;
     float mid[NT][4];
     if (P::kPrecise) {
       constexpr uint32_t kMinus = 0x81e081e0u;  // -480 * 2^-24: -7.5 in units of 2^-18
@@ -594,7 +598,7 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
       const uint32_t sel = half ? 0x7632u : 0x5410u;
       uint32_t x[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) codes<P::kPrecise>(__byte_perm(w[i], w[i + 4], sel), x[i]);
+      for (int i = 0; i < 4; ++i) codes<P::kPrecise>(__byte_perm(w[i], w[i + 4], sel), x[i], flip);
 #pragma unroll
       for (int m2 = 0; m2 < 2; ++m2)
 #pragma unroll
@@ -606,8 +610,13 @@ __device__ __forceinline__ void accumulate(Acc<D, MODE>& A, const unsigned char*
           else mma(c, a0, bf[nt][0], bf[nt][1], 0.f, 0.f, 0.f, 0.f);
           mma(c, a1, bf[nt][2], bf[nt][3], c[0], c[1], c[2], c[3]);
           float(&o)[4] = A.o[g][2 * half + m2][nt];
-          add2(o[0], o[1], c[0], c[1]);
-          add2(o[2], o[3], c[2], c[3]);
+          if (P::kPrecise) {
+            add2(o[0], o[1], c[0], c[1], sign);
+            add2(o[2], o[3], c[2], c[3], sign);
+          } else {
+            add2(o[0], o[1], c[0], c[1]);
+            add2(o[2], o[3], c[2], c[3]);
+          }
         }
     }
   }
@@ -987,13 +996,23 @@ cudaError_t pick_attention(const AttnArgs& a, bool others, int num_sms, cudaStre
   return cols <= 4 ? pick_feat<D, FP32_4>(a, others, num_sms, st) : pick_feat<D, FP32_8>(a, others, num_sms, st);
 }
 
-// Query rows per KV head from which on a sequence goes to the prompt kernel.
-constexpr int kPromptRows = 33;
+// Query rows per KV head from which on a sequence goes to the prompt kernel.  That one takes 256 query rows at a time
+// and 26 to 38 us however few keys there are; the decode kernel's time grows with rows x keys, 8 or 16 query rows at a
+// time.  Measured (us, decode / prompt; with N the (sequence, KV head) pairs and R the rows):
+//   fp32 d 64, N 3:    R 512 at 510 rows 14 / 38;   R 4096 at 255 21 / 40, at 510 32 / 40;  R 32768 at 159 58 / 66, at 255 85 / 67
+//   fp32 d 64, N 48:   R 512 at 192 37 / 46, at 318 52 / 51;   R 2048 at 126 56 / 63, at 192 78 / 61
+//   bf16 d 64, N 128:  R 512 at 96 34 / 37, at 160 47 / 38;    R 2048 at 160 94 / 107, at 256 140 / 111
+//   bf16 d 128, N 8:   R 512 at 512 26 / 34;   R 4096 at 192 35 / 40, at 320 46 / 48;       R 32768 at 128 108 / 109
+//   bf16 d 128, N 128: R 512 at 64 40 / 46, at 128 61 / 47
+// so the border is near 100 query rows where there is much to do and moves up as 1 / (N R).
+long long prompt_rows(const Kv4Geom& g, const Kv4Batch& b) {
+  return 96 + (1ll << 22) / ((long long)b.n_seq * g.nkv * std::max(1, b.max_rows));
+}
 
 // Whether the batch may have a sequence for the prompt kernel (fp32 at head dim 128 would need two accumulators and
 // operands twice as large per tile: the decode kernel takes it).
 bool has_prompts(const Kv4Geom& g, const Kv4Batch& b, int bf16) {
-  return (long long)b.max_count * (g.nq / g.nkv) >= kPromptRows && (bf16 || g.d == 64);
+  return (long long)b.max_count * (g.nq / g.nkv) >= prompt_rows(g, b) && (bf16 || g.d == 64);
 }
 // The workspace: the decode kernel's partials, the prompt kernel's, lse.
 size_t own_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
@@ -1002,7 +1021,7 @@ size_t own_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
 }
 size_t part_bytes(const Kv4Geom& g, const Kv4Batch& b, int num_sms) {
   return own_bytes(g, b, num_sms) +
-         ((long long)b.max_count * (g.nq / g.nkv) >= kPromptRows ? round256(kv4_prompt_partials(g, b, num_sms)) : 0);
+         ((long long)b.max_count * (g.nq / g.nkv) >= prompt_rows(g, b) ? round256(kv4_prompt_partials(g, b, num_sms)) : 0);
 }
 
 }  // namespace
@@ -1011,7 +1030,8 @@ size_t kv4_attention_workspace(const Kv4Geom& g, const Kv4Batch& b, int num_sms)
   return part_bytes(g, b, num_sms) + (g.track ? round256((size_t)b.n_tokens * g.nq * 4) : 0);
 }
 
-cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const Kv4Attn& at, void* ws, int num_sms, cudaStream_t st) {
+cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, Kv4Attn at, void* ws, int num_sms, cudaStream_t st) {
+  if (!g.track) at.window = std::min(at.window, 1 << 28);  // row numbers are below 2^27: no more than all, and sums stay in 32 bits
   AttnArgs a;
   a.g = g;
   a.b = b;
@@ -1029,7 +1049,7 @@ cudaError_t kv4_attention(const Kv4Geom& g, int layer, const Kv4Batch& b, const 
   const bool prompts = has_prompts(g, b, at.bf16);
   if (prompts) {
     // a sequence alone goes to the prompt kernel however few its tokens turn out to be
-    a.below = b.n_seq == 1 ? 1 : kPromptRows;
+    a.below = b.n_seq == 1 ? 1 : (int)prompt_rows(g, b);
     uint8_t* part = reinterpret_cast<uint8_t*>(ws) + own_bytes(g, b, num_sms);
     if (cudaError_t e = kv4_prompt(g, layer, b, at, a.below, reinterpret_cast<float*>(part), a.lse, num_sms, st)) return e;
   }

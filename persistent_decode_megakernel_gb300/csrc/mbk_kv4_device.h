@@ -118,21 +118,26 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+// (a, b) += s (c, d) in one instruction.
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d, float s) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %4};\n fma.rn.f32x2 x, y, z, x;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b) : "f"(c), "f"(d), "f"(s));
+}
 // (a, b) += (c, d) in one instruction.
 __device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
   asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
       : "+f"(a), "+f"(b) : "f"(c), "f"(d));
 }
 // The codes of a word as four operand registers (codes i and i + 4 in register i), in units of
-// 2^-24 (16 times that in registers 1 and 3), with PRECISE of 2^-18.
+// 2^-24 (16 times that in registers 1 and 3), with PRECISE of 2^-18.  flip (PRECISE): 0, or all ones for 15 - code.
 template <bool PRECISE>
-__device__ __forceinline__ void codes(uint32_t x, uint32_t (&r)[4]) {
+__device__ __forceinline__ void codes(uint32_t x, uint32_t (&r)[4], uint32_t flip = 0u) {
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kTop = 0x03c003c0u;
   if (PRECISE) {
-    r[0] = (x << 6) & kTop;
-    r[1] = (x << 2) & kTop;
-    r[2] = (x >> 2) & kTop;
-    r[3] = (x >> 6) & kTop;
+    r[0] = ((x << 6) ^ flip) & kTop;
+    r[1] = ((x << 2) ^ flip) & kTop;
+    r[2] = ((x >> 2) ^ flip) & kTop;
+    r[3] = ((x >> 6) ^ flip) & kTop;
   } else {
     const uint32_t x8 = x >> 8;
     r[0] = x & kLow;

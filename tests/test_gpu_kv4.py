@@ -35,7 +35,8 @@ class Setup:
         self.rows, self.counts = list(rows), list(counts)
         self.offsets = [0] + np.cumsum(counts).tolist()
         need = [-(-max(r, 1) // page) for r in rows]
-        self.max_pages = max(need) + 1
+        # a table that may reach far makes prompts of few tokens worth the prompt kernel
+        self.max_pages = 2 ** 17 // page if max(counts) * heads >= 64 * kv else max(need) + 1
         perm = rng.permutation(sum(need) + spare)
         self.tables = np.full((len(rows), self.max_pages), -7, np.int32)  # entries behind the last page are never read
         at = 0
@@ -388,7 +389,7 @@ def test_decode_with_eviction_step_by_step():
     heads, kv, d, keep, recent = 6, 2, 64, 40, 8
     s = Setup([30, 50], [30, 50], heads, kv, d, page=32, track=True, layers=1, layer=0, fill=False, spare=6)
     ref, rows, nxt = s.pool, [0, 0], [0, 0]
-    s.tables[:, :] = np.arange(2 * s.max_pages).reshape(2, -1)
+    s.tables[:, :3] = np.arange(6).reshape(2, -1)
     s.dev["tables"].copy_(torch.from_numpy(s.tables))
     counts = [30, 50]
     for step in range(14):
@@ -453,7 +454,7 @@ def test_scales(heads, dtype, scale):
 
 
 @pytest.mark.parametrize("heads,dtype", [((9, 3, 64), torch.float32), ((4, 2, 128), torch.bfloat16), ((4, 2, 128), torch.float32)], ids=str)
-@pytest.mark.parametrize("counts", [[10, 11, 12], [32, 33, 1], [17], [16], [8]], ids=str)
+@pytest.mark.parametrize("counts", [[10, 11, 12], [32, 33, 1], [17], [16], [8], [34, 35, 36], [48, 56, 64], [56], [40]], ids=str)
 def test_around_the_border_between_the_kernels(heads, dtype, counts):
     """Query rows per KV head just below and above the prompt kernel's least, one sequence and several."""
     s = Setup([c + 45 for c in counts], counts, *heads, track=True, gap=1)
@@ -632,14 +633,16 @@ def test_nan_rows_under_a_prompt(heads, dtype, window):
     check(torch.from_numpy(np.nan_to_num(got)), np.nan_to_num(want), good.tolerance(q, dtype), "others")
 
 
+@pytest.mark.parametrize("window", [0, 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("counts", [[60, 40, 50], [10, 1, 2]], ids=["prompts", "few"])
 @pytest.mark.parametrize("heads,dtype", PROMPTS, ids=str)
-def test_more_new_tokens_than_rows(heads, dtype):
-    """The first tokens see no row: zero; a sequence without rows and one that sees all."""
-    s = Setup([20, 0, 70], [60, 40, 50], *heads)
+def test_more_new_tokens_than_rows(heads, dtype, counts, window):
+    """The first tokens see no row: zero; a sequence without rows and one that sees all; the largest window."""
+    s = Setup([counts[0] // 3, 0, 70], counts, *heads)
     q = s.q(dtype)
-    want, _ = s.expect(q)
-    assert (want[:40] == 0).all() and (want[60:100] == 0).all()
-    check(_run(s, q, {}), want, s.tolerance(q, dtype), "out")
+    want, _ = s.expect(q, window=window)
+    assert (want[:counts[0] - counts[0] // 3] == 0).all() and (want[counts[0]:counts[0] + counts[1]] == 0).all()
+    check(_run(s, q, dict(window=window)), want, s.tolerance(q, dtype), "out")
 
 
 @pytest.mark.parametrize("heads,dtype", PROMPTS, ids=str)
