@@ -13,7 +13,8 @@
 // the weights are rounded to fp16 too.
 //   fp32 (head dim 64): the operands are code - 8, exact; q and the weights are hi + lo fp16 (22 bits); the
 // softmax applies the rows' scale and lo, as the decode kernel does.  The tensor cores' sums are truncated, so the
-// output is moved to a second buffer and added there in fp32 every 8 tiles.
+// output is moved to a second buffer and added there in fp32 every 8 tiles; and as the truncation leaves a bias in each such
+// group (which reached 3.6e-5 of the output at 130,000 rows), every other group takes 15 - code and is subtracted.
 //   Bound by the softmax's instructions, which therefore go two values at a time where the GPU has a form for it.
 #include "mbk_kv4_device.h"
 #include "mbk_kv4_split.h"
@@ -27,6 +28,8 @@ constexpr int kKeys = 64;      // cache rows of a key tile: one 128-byte row of 
 constexpr int kThreads = 512;  // softmax 2 x 128, K 128, V 128
 constexpr int kTmemCols = 512; // per query tile: scores 2 x 64, output 64 or 128, fp32: sums 64
 constexpr int kFlush = 8;      // fp32: tiles between two moves of the output
+// fp32: every other such group takes V's codes from above (15 - code) and is subtracted, see the top.
+__device__ __forceinline__ bool odd_group(int j) { return j / kFlush & 1; }
 constexpr int kMaxRounds = 4;  // items per CTA at most, about, where keys are split
 constexpr int kNotes = 4;      // tiles whose notes and pairs are kept
 constexpr float kSlack = 8.f;  // a running maximum is renewed when a score exceeds it by 2^8
@@ -378,7 +381,7 @@ struct RawV {
 // K of a tile to its stage, and what the softmax has to know: positions, bad pages, V's NaN rows, fp32: the pairs.
 template <int D, bool FP32>
 __device__ __forceinline__ void convert_k(const RawK<D>& w, const PromptArgs& a, unsigned char* kst, unsigned char* smem, int slot, int row0,
-                                          int rows, int t, TileNote* note) {
+                                          int rows, int t, bool odd, TileNote* note) {
   using L = Layout<D, FP32>;
   constexpr int kGroups = D / 64;
   const int key = t >> 1, half = t & 1;
@@ -404,7 +407,7 @@ __device__ __forceinline__ void convert_k(const RawK<D>& w, const PromptArgs& a,
     }
   }
   if (FP32) {
-    // the rows' pairs, lo moved to the codes' middle, and V's largest scale
+    // the rows' pairs, lo moved to the codes' middle (odd groups count 7 - code), and V's largest scale
     float* pairs = reinterpret_cast<float*>(smem + L::kPairsAt) + slot * 4 * kKeys;
     if (half == 0) {
       const float2 p = unpack_half(kon ? w.kp[0] : 0u);
@@ -414,7 +417,7 @@ __device__ __forceinline__ void convert_k(const RawK<D>& w, const PromptArgs& a,
     if (t < 64) {
       const float2 p = unpack_half(vp);
       pairs[2 * kKeys + t] = p.x;
-      pairs[3 * kKeys + t] = fmaf(8.f, p.x, p.y);
+      pairs[3 * kKeys + t] = fmaf(odd ? 7.f : 8.f, p.x, p.y);
       const unsigned e = __reduce_max_sync(0xffffffffu, (vp >> 10) & 31u);
       if ((t & 31) == 0) note->e[t >> 5] = min((int)e - 15, 15);
     }
@@ -422,9 +425,10 @@ __device__ __forceinline__ void convert_k(const RawK<D>& w, const PromptArgs& a,
   if (a.g.track && half == 0) reinterpret_cast<int*>(smem + L::kPosAt)[slot * kKeys + key] = w.pos;
 }
 
-// V of a tile to its stage, transposed: of rows vk .. vk + 3, 8 bytes of each of 8 dims' rows.
+// V of a tile to its stage, transposed: of rows vk .. vk + 3, 8 bytes of each of 8 dims' rows.  flip (fp32): 0, or all
+// ones for 15 - code.
 template <int D, bool FP32>
-__device__ __forceinline__ void convert_v(const RawV<D>& w, unsigned char* vst, int row0, int rows, int t) {
+__device__ __forceinline__ void convert_v(const RawV<D>& w, unsigned char* vst, int row0, int rows, int t, uint32_t flip) {
   constexpr int kGroups = D / 64;
   const int vk = 4 * (t & 15), vw = t >> 4;
 #pragma unroll
@@ -445,8 +449,8 @@ __device__ __forceinline__ void convert_v(const RawV<D>& w, unsigned char* vst, 
     for (int hf = 0; hf < 2; ++hf) {
       const uint32_t sel = hf ? 0x7632u : 0x5410u;
       __half2 x[4], y[4];
-      code_pairs<FP32>(__byte_perm(w.v[g][0], w.v[g][1], sel), x);
-      code_pairs<FP32>(__byte_perm(w.v[g][2], w.v[g][3], sel), y);
+      code_pairs<FP32>(__byte_perm(w.v[g][0], w.v[g][1], sel) ^ flip, x);
+      code_pairs<FP32>(__byte_perm(w.v[g][2], w.v[g][3], sel) ^ flip, y);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int dim = 4 * hf + j;  // row of the tile: g * 64 + 8 vw + dim; its low three bits are dim
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const int st = tile_no & 1, slot = tile_no % kNotes;
           w.bad &= k * kKeys + kRows < sq.r ? 3u : 1u;  // a block behind the cache's end has no page: not an error
           if (tile_no >= 2 && !warp_wait(&k_empty[st], ((tile_no >> 1) - 1) & 1, abort)) return false;
-          convert_k<D, FP32>(w, a, smem + L::kKAt + st * L::kTile, smem, slot, k * kKeys, sq.r, t, &notes[slot]);
+          convert_k<D, FP32>(w, a, smem + L::kKAt + st * L::kTile, smem, slot, k * kKeys, sq.r, t, odd_group(k - it.k0), &notes[slot]);
           fence_async();
           mbar_arrive(&k_full[st]);
           return warp != 8 || (score(tile_no, k - it.k0) && (k == it.k0 || product(tile_no - 1, k - it.k0 - 1)));
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         run(cur, nxt, [&](RawV<D>& w, int k) {
           const int st = tile_no & 1;
           if (tile_no >= 2 && !warp_wait(&v_empty[st], ((tile_no >> 1) - 1) & 1, abort)) return false;
-          convert_v<D, FP32>(w, smem + L::kVAt + st * L::kTile, k * kKeys, sq.r, t);
+          convert_v<D, FP32>(w, smem + L::kVAt + st * L::kTile, k * kKeys, sq.r, t, FP32 && odd_group(k - it.k0) ? ~0u : 0u);
           fence_async();
           mbar_arrive(&v_full[st]);
           return true;
@@ -814,12 +818,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (flush) {  // moved to the sums
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
+              const float sign = odd_group(j - 1) ? -1.f : 1.f;
               float o[16], s[16];
               tmem_ld16(t_out + c, o);
               if (j > kFlush) tmem_ld16(t_sum + c, s);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = (j > kFlush ? o[e] + s[e] : o[e]) * rescale;
+              for (int e = 0; e < 16; ++e) o[e] = (j > kFlush ? fmaf(sign, o[e], s[e]) : o[e]) * rescale;
               tmem_st16(t_sum + c, o);
             }
           } else {
@@ -873,6 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       // the output, or the run's partial
       const bool last = it.parts <= 1;
+      const float sign = FP32 && n > 0 && odd_group(n - 1) ? -1.f : 1.f;
       const float sum_l = halves(l).x + halves(l).y, sum_z = halves(z).x + halves(z).y;
       const float inv = last ? (sum_l > 0.f || sum_l != sum_l ? 1.f / sum_l : 0.f) : 1.f;
       const float m_ref = m + (FP32 ? (float)(e_cur - 6) : 0.f);  // what l and the output are relative to
@@ -897,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             f2 x = n > 0 ? o[2 * c + e] : 0ull;
-            if (FP32 && n > kFlush) x = sum2(x, s[2 * c + e]);
+            if (FP32 && n > kFlush) x = fma2(x, pair_of(sign, sign), s[2 * c + e]);
             if (FP32) x = sum2(x, pair_of(sum_z, sum_z));
             const float2 u = halves(mul2(x, pair_of(inv, inv)));
             y[2 * e] = bad ? NAN : n > 0 ? u.x : 0.f;
