@@ -7,15 +7,19 @@
 // instructions in between; and a thread of the other eight warps owns a query row: it reads the row's scores from
 // tensor memory, keeps its softmax and writes its weights over the scores, where the second product takes them
 // from.  Scores have two buffers and K and V two stages, so that conversion and tensor cores work one tile
-// ahead of the softmax.  (Two CTAs of one query tile and four conversion warps each were slower, 400 us against the
-// time in the table: the conversion held the softmax up.)
+// ahead of the softmax.  (Two CTAs of one query tile and four conversion warps each were slower, 400 us where this form
+// then took 246: the conversion held the softmax up.)
 //   bf16: K and V are the values lo + scale * code rounded to fp16 (one rounding, 2^-11; bf16 has 2^-8),
 // the weights are rounded to fp16 too.
 //   fp32 (head dim 64): the operands are code - 8, exact; q and the weights are hi + lo fp16 (22 bits); the
 // softmax applies the rows' scale and lo, as the decode kernel does.  The tensor cores' sums are truncated, so the
-// output is moved to a second buffer and added there in fp32 every 8 tiles; and as the truncation leaves a bias in each such
+// output is moved to a second buffer and added there in fp32 every 2 tiles; and as the truncation leaves a bias in each such
 // group (which reached 3.6e-5 of the output at 130,000 rows), every other group takes 15 - code and is subtracted.
-//   Bound by the softmax's instructions, which therefore go two values at a time where the GPU has a form for it.
+//   Bound by the softmax, which therefore goes two values at a time where the GPU has a form for it: of some 4,600 clocks a
+// key tile (both query tiles) 1,300 are scale and maximum and 2,500 exponentials, split and store, two warps a scheduler
+// that wait for their own results (issue slots 39% busy, tensor cores 16%).  Measured: the last 2,048 tokens of 8,192 rows,
+// 9 and 3 heads, d 64, fp32: 228 us with the join, 148 TFLOP/s of the formula's; four prompts of up to 1,024 tokens over up
+// to 4,096 rows, 32 and 8 heads, d 128, bf16, cap and window: 363 us.
 #include "mbk_kv4_device.h"
 #include "mbk_kv4_split.h"
 
@@ -27,7 +31,9 @@ constexpr int kItem = 256;     // query rows of an item: two tiles
 constexpr int kKeys = 64;      // cache rows of a key tile: one 128-byte row of fp16
 constexpr int kThreads = 512;  // softmax 2 x 128, K 128, V 128
 constexpr int kTmemCols = 512; // per query tile: scores 2 x 64, output 64 or 128, fp32: sums 64
-constexpr int kFlush = 8;      // fp32: tiles between two moves of the output
+// fp32: tiles between two moves of the output.  Measured at 20,000 rows, queries of 0.3 (fp32 arithmetic itself: 5.5e-7 off):
+// every 8 2.0e-6 off, 4 9e-7, 2 5.4e-7; the last 2,048 tokens of 8,192 rows in 217, 222 and 231 us.
+constexpr int kFlush = 2;
 // fp32: every other such group takes V's codes from above (15 - code) and is subtracted, see the top.
 __device__ __forceinline__ bool odd_group(int j) { return j / kFlush & 1; }
 constexpr int kMaxRounds = 4;  // items per CTA at most, about, where keys are split

@@ -726,3 +726,24 @@ def test_query_tiles_that_run_ahead_of_each_other(heads, dtype, counts):
         # scores below 8 in size: weights off by 8 (2^-22 + 11 2^-23); bf16: out 2^-8, weights and V 2^-11 each, K 2^-11 of a score's terms
         tol = 2.0 ** -16 if dtype == torch.float32 else 2.0 ** -8 + 3 * 2.0 ** -11
         assert (first[at:at + c].double() - want).norm() <= tol * want.norm()
+
+
+@pytest.mark.parametrize("size", [0.3, 1.0, 2.0])
+@pytest.mark.parametrize("count", [1, 1024], ids=["decode", "prompt"])
+def test_fp32_is_as_exact_as_fp32_arithmetic(count, size):
+    """Over 30,000 rows, whose average is small against them: at most twice as far off as the same formula in fp32."""
+    nq, kv, d, rows = 6, 2, 64, 30000
+    cache, every, batch, q = _random_cache(nq, kv, d, 1, rows, [count], torch.float32)
+    q *= size
+    got = cache.attention(0, batch, q).double()
+    k, v = cache.read(0, every)
+    sums = [0.0, 0.0, 0.0]
+    for h in range(nq):
+        out = []
+        for t in (torch.float64, torch.float32):
+            x = (q[:, h].to(t) @ k[:, h * kv // nq].to(t).T) * d ** -0.5
+            x = x.masked_fill(torch.ones(count, rows, dtype=torch.bool, device="cuda").triu(rows - count + 1), -np.inf)
+            out.append((x.softmax(-1) @ v[:, h * kv // nq].to(t)).double())
+        for i, x in enumerate((got[:, h] - out[0], out[1] - out[0], out[0])):
+            sums[i] += float(x.square().sum())
+    assert sums[0] ** 0.5 <= 2 * sums[1] ** 0.5, [(x / sums[2]) ** 0.5 for x in sums]
